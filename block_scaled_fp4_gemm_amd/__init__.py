@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -46,6 +47,12 @@ _SIGS = {
     "gemm_fp4_blockscaled_splitk": [_p, _p, _p, _p, _p, _p, _sz, _u32, _u32, _u32, _u32, _p],
     "fp4_scales_from_blocked": [_p, _p, _u32, _u32, _u32, _p],
     "bf16_scaled_add": [_p, _p, _sz, _f32, _p],
+    "mxfp4_quantize": [_p, ctypes.c_int, _u32, _p, _p, _p, _u32, _u32, _u32, _p],
+    "mxfp4_dequantize": [_p, _p, _p, ctypes.c_int, _u32, _u32, _p],
+    "gemm_mxfp4": [_p, _p, _p, _p, _p, _u32, _u32, _u32, _p],
+    "gemm_mxfp4_grouped": [_p, _p, _p, _p, _p, _p, _u32, _u32, _u32, _u32, _p],
+    "moe_route": [_p, ctypes.c_int, _p, _p, _p, _sz, _u32, _u32, _u32, ctypes.c_int, _p],
+    "moe_route_backward": [_p, ctypes.c_int, _p, _p, _p, _p, _p, _p, _p, _u32, _u32, _u32, ctypes.c_int, _p],
 }
 for _name, _args in _SIGS.items():
     try:
@@ -57,6 +64,8 @@ for _name, _args in _SIGS.items():
     _fn.restype = ctypes.c_int
 lib.gemm_bf16_splitk_workspace_bytes.argtypes = [_u32, _u32, _u32]
 lib.gemm_bf16_splitk_workspace_bytes.restype = ctypes.c_size_t
+lib.moe_route_workspace_bytes.argtypes = [_u32, _u32]
+lib.moe_route_workspace_bytes.restype = ctypes.c_size_t
 lib.bg_status_string.argtypes = [ctypes.c_int]
 lib.bg_status_string.restype = ctypes.c_char_p
 lib.bg_tune_set.argtypes = [ctypes.c_int, ctypes.c_int]
@@ -67,7 +76,7 @@ lib.bg_tile_map.argtypes = [ctypes.c_int, _u32, _u32, _p, _p]
 lib.bg_tile_map.restype = ctypes.c_int
 
 EXPORTS = tuple(_SIGS) + ("gemm_bf16_splitk_workspace_bytes", "bg_status_string", "bg_tune_set", "bg_tune_get",
-                          "bg_tile_map")
+                          "bg_tile_map", "moe_route_workspace_bytes")
 
 BG_OK, BG_ERR_NULL, BG_ERR_SHAPE, BG_ERR_ALIGN, BG_ERR_WORKSPACE, BG_ERR_ALIAS, BG_ERR_DEVICE, \
     BG_ERR_LAUNCH = range(8)
@@ -478,6 +487,216 @@ def bf16_scaled_add(out: torch.Tensor, delta: torch.Tensor, scale: float, stream
     _on_device(out, delta)
     _check(lib.bf16_scaled_add(_ptr(out), _ptr(delta), out.numel(), float(scale), _stream(stream)),
            "bf16_scaled_add")
+    return out
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for a call on `stream` (None: the current one). Memory of
+    torch's pool belongs to the stream it was taken on: taken on another one,
+    it could still be in use there, or be handed out there again while the
+    call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+# ---------------------------------------------------------------------------
+# MXFP4: E2M1 elements, one E8M0 scale per 32 of them
+# ---------------------------------------------------------------------------
+
+_BG_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # bg_type
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    _tensor(t, what)
+    if t.dtype not in _BG_TYPES:
+        raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    return _BG_TYPES[t.dtype]
+
+
+def _i32(t: torch.Tensor, what: str) -> torch.Tensor:
+    _tensor(t, what)
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what}: expected int32, got {t.dtype}")
+    return t
+
+
+def _blocks32(k: int) -> None:
+    if k % 32 != 0:
+        raise ValueError(f"K = {k} must be a multiple of 32 (one scale per 32 elements)")
+
+
+def _mx_operands(a, sfa, b, sfb, experts: bool):
+    """Shapes of MXFP4 operands: A [M, K/2], SFA [M, K/32], B [(E,) N, K/2], SFB [(E,) N, K/32]."""
+    m, kh = _dims(_bytes(a, "A"), 2, "A")
+    _dims(_bytes(b, "B"), 3 if experts else 2, "B")
+    k = 2 * kh
+    _blocks32(k)
+    lead = tuple(b.shape[:-1])
+    _shape(b, (*lead, kh), "B")
+    _shape(_bytes(sfa, "SFA"), (m, k // 32), "SFA")
+    _shape(_bytes(sfb, "SFB"), (*lead, k // 32), "SFB")
+    return lead, m, k
+
+
+def mxfp4_quantize(x: torch.Tensor, rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   scales: torch.Tensor | None = None, stream=None):
+    """(codes [R, K/2], scales [R, K/32]) of x [M, K] (bfloat16 or float32, contiguous rows at any row
+    stride). With `rows` (int32 [R]), row i of the result is x[rows[i]], all zero where rows[i] is not a
+    row of x; without, R = M."""
+    kind = _type(x, "x")
+    _dims(x, 2, "x")
+    m, k, ldx = _rows(x, "x")
+    _blocks32(k)
+    r = m
+    if rows is not None:
+        (r,) = _dims(_i32(rows, "rows"), 1, "rows")
+    if out is None:
+        out = _empty((r, k // 2), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((r, k // 32), torch.uint8, x.device, stream)
+    _shape(_bytes(out, "out"), (r, k // 2), "out")
+    _shape(_bytes(scales, "scales"), (r, k // 32), "scales")
+    _on_device(x, rows, out, scales)
+    if r == 0:      # an empty row list has no address, which the library would take for no list
+        return out, scales
+    _check(lib.mxfp4_quantize(x.data_ptr(), kind, ldx, _ptr(rows), _ptr(out), _ptr(scales), m, r, k,
+                              _stream(stream)), "mxfp4_quantize")
+    return out, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                     out: torch.Tensor | None = None, stream=None):
+    """The values [M, K] of MXFP4 codes [M, K/2] and scales [M, K/32], as bfloat16 or float32."""
+    m, kh = _dims(_bytes(codes, "codes"), 2, "codes")
+    k = 2 * kh
+    _blocks32(k)
+    _shape(_bytes(scales, "scales"), (m, k // 32), "scales")
+    if out is None:
+        out = _empty((m, k), dtype, codes.device, stream)
+    kind = _type(out, "out")
+    _shape(out, (m, k), "out")
+    _on_device(codes, scales, out)
+    _check(lib.mxfp4_dequantize(_ptr(codes), _ptr(scales), _ptr(out), kind, m, k, _stream(stream)),
+           "mxfp4_dequantize")
+    return out
+
+
+def gemm_mxfp4(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
+               out: torch.Tensor | None = None, stream=None):
+    """C = bf16(deq(A) @ deq(B)^T): A [M, K/2] packed e2m1, SFA [M, K/32] e8m0, B [N, K/2], SFB [N, K/32]."""
+    (n,), m, k = _mx_operands(a, sfa, b, sfb, experts=False)
+    if out is None:
+        out = _empty((m, n), torch.bfloat16, a.device, stream)
+    _shape(_bits16(out, "out"), (m, n), "out")
+    _on_device(a, sfa, b, sfb, out)
+    _check(lib.gemm_mxfp4(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(out), m, n, k, _stream(stream)),
+           "gemm_mxfp4")
+    return out
+
+
+def gemm_mxfp4_grouped(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
+                       offsets: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    """Rows offsets[e] .. offsets[e+1]-1 of A [S, K/2] times expert e of B [E, N, K/2] (scales SFA [S, K/32],
+    SFB [E, N, K/32], offsets int32 [E + 1] on the device) -> bf16 [S, N]. Rows before offsets[0] and from
+    offsets[E] on are not written."""
+    (e, n), s, k = _mx_operands(a, sfa, b, sfb, experts=True)
+    _shape(_i32(offsets, "offsets"), (e + 1,), "offsets")
+    if out is None:
+        out = _empty((s, n), torch.bfloat16, a.device, stream)
+    _shape(_bits16(out, "out"), (s, n), "out")
+    _on_device(a, sfa, b, sfb, offsets, out)
+    _check(lib.gemm_mxfp4_grouped(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(offsets), _ptr(out), s, n, k, e,
+                                  _stream(stream)), "gemm_mxfp4_grouped")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Expert routing
+# ---------------------------------------------------------------------------
+
+class MoeRouting(NamedTuple):
+    """What moe_route decides (see include/blockgemm.h): device tensors, and the two arguments that
+    moe_route_backward needs again."""
+    ids: torch.Tensor          # int32 [T, k], -1: no choice
+    weights: torch.Tensor      # float32 [T, k]
+    counts: torch.Tensor       # int32 [E]
+    offsets: torch.Tensor      # int32 [E + 1]
+    rows: torch.Tensor         # int32 [T * k]: the row at every place, -1 behind the last
+    pos: torch.Tensor          # int32 [T, k]: the place of every choice, -1: none
+    mean_probs: torch.Tensor   # float32 [E]
+    loss: torch.Tensor         # float32 scalar
+    n_valid: torch.Tensor      # int32 scalar
+    k: int
+    normalize: bool
+
+
+class _RoutingPointers(ctypes.Structure):
+    _fields_ = [(f, _p) for f in MoeRouting._fields[:9]]
+
+
+def moe_route_workspace_bytes(t: int, e: int) -> int:
+    return int(lib.moe_route_workspace_bytes(t, e))
+
+
+def moe_route(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None, normalize: bool = True,
+              workspace: torch.Tensor | None = None, stream=None) -> MoeRouting:
+    """Top-k routing of router logits [T, E] (bfloat16 or float32): choices, weights, per-expert counts, the
+    dispatch order and the balance loss. `valid` (bool or byte [T]) leaves rows out. `workspace` is a byte
+    tensor of moe_route_workspace_bytes(T, E) bytes (allocated if None)."""
+    kind = _type(logits, "logits")
+    t, e = _dims(logits, 2, "logits")
+    if not 1 <= k <= min(e, 16):
+        raise ValueError(f"k = {k} must lie in 1 .. min(E, 16) = {min(e, 16)}")
+    if valid is not None:
+        _tensor(valid, "valid")
+        if valid.element_size() != 1 or valid.is_floating_point():
+            raise TypeError(f"valid: expected bool or bytes, got {valid.dtype}")
+        _shape(valid, (t,), "valid")
+    _on_device(logits, valid, workspace)
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if workspace is None:
+        need = moe_route_workspace_bytes(t, e)
+        workspace = _empty(need, torch.uint8, dev, stream) if need else None
+    r = MoeRouting(_empty((t, k), i32, dev, stream), _empty((t, k), f32, dev, stream),
+                   _empty(e, i32, dev, stream), _empty(e + 1, i32, dev, stream),
+                   _empty(t * k, i32, dev, stream), _empty((t, k), i32, dev, stream),
+                   _empty(e, f32, dev, stream), _empty((), f32, dev, stream),
+                   _empty((), i32, dev, stream), k, bool(normalize))
+    ptrs = _RoutingPointers(*[x.data_ptr() for x in r[:9]])
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.moe_route(_ptr(logits), kind, _ptr(valid), ctypes.byref(ptrs), _ptr(workspace), ws_bytes, t, e, k,
+                         int(r.normalize), _stream(stream)), "moe_route")
+    return r
+
+
+def moe_route_backward(logits: torch.Tensor, routing: MoeRouting, dweights: torch.Tensor | None = None,
+                       dloss: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+    """The gradient of the logits, for gradients of routing.weights (float32 [T, k]) and of routing.loss (one
+    float32); None is zero. `out` may be the logits."""
+    kind = _type(logits, "logits")
+    t, e = _dims(logits, 2, "logits")
+    _shape(_i32(routing.ids, "ids"), (t, routing.k), "ids")
+    _shape(_f32(routing.weights, "weights"), (t, routing.k), "weights")
+    _shape(_i32(routing.counts, "counts"), (e,), "counts")
+    if _i32(routing.n_valid, "n_valid").numel() != 1:
+        raise ValueError(f"n_valid must hold one value, got shape {tuple(routing.n_valid.shape)}")
+    if dweights is not None:
+        _shape(_f32(dweights, "dweights"), (t, routing.k), "dweights")
+    if dloss is not None and _f32(dloss, "dloss").numel() != 1:
+        raise ValueError(f"dloss must hold one value, got shape {tuple(dloss.shape)}")
+    if out is None:
+        out = _empty((t, e), logits.dtype, logits.device, stream)
+    if _type(out, "out") != kind:
+        raise TypeError(f"out: expected {logits.dtype}, got {out.dtype}")
+    _shape(out, (t, e), "out")
+    _on_device(logits, routing.ids, routing.weights, routing.counts, routing.n_valid, dweights, dloss, out)
+    _check(lib.moe_route_backward(_ptr(logits), kind, _ptr(routing.ids), _ptr(routing.weights), _ptr(routing.counts),
+                                  _ptr(routing.n_valid), _ptr(dweights), _ptr(dloss), _ptr(out), t, e, routing.k,
+                                  int(routing.normalize), _stream(stream)), "moe_route_backward")
     return out
 
 

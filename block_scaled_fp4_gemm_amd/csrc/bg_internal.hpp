@@ -55,6 +55,74 @@ struct W4a16Problem {
     uint32_t ldbt;       // 0: B [N, K/2], SFB [N, K/16]; else B [K/2, ldbt], SFB [K/16, ldbt] (transposed)
 };
 
+struct MxQuantProblem {
+    const void* x;         // [M, K] of type, rows ldx elements apart
+    const int32_t* rows;   // [R] source rows, or NULL (row i is row i)
+    uint8_t* codes;        // [R, K/2]
+    uint8_t* scales;       // [R, K/32]
+    uint32_t M, R, K, ldx;
+    int type;              // bg_type of x
+};
+
+struct MxGemmProblem {
+    const uint8_t* A;      // [M, K/2] packed e2m1
+    const uint8_t* SFA;    // [M, K/32] e8m0
+    const uint8_t* B;      // [E][N, K/2]
+    const uint8_t* SFB;    // [E][N, K/32]
+    uint16_t* C;           // [M, N] bf16
+    uint32_t M, N, K;
+    const int32_t* offsets;   // [E + 1] row ranges of the experts, or NULL (one product of all rows)
+    uint32_t E;
+    uint32_t cus;          // compute units of the device (tile choice)
+};
+
+struct RouteProblem {
+    const void* logits;    // [T, E] of type
+    int type;              // bg_type of the logits
+    const uint8_t* valid;  // [T] or NULL
+    bg_moe_routing out;
+    void* ws;              // route_workspace_bytes(T, E)
+    uint32_t T, E, k;
+    int normalize;
+};
+
+struct RouteBackwardProblem {
+    const void* logits;    // [T, E] of type
+    int type;
+    const int32_t* ids;
+    const float* weights;
+    const int32_t* counts;
+    const int32_t* n_valid;
+    const float* dweights;   // [T, k] or NULL
+    const float* dloss;      // [1] or NULL
+    void* dlogits;         // [T, E] of type
+    uint32_t T, E, k;
+    int normalize;
+};
+
+constexpr uint32_t kMaxExperts = 1024;   // routing and grouped products
+constexpr uint32_t kMaxTopK = 16;
+
+// Rows per workgroup of moe_route: 16 at least (one pass of a workgroup), and
+// for long batches more, at most 128, so that the per-workgroup counts and
+// sums that the workspace holds stay small against the logits.
+inline uint32_t route_rows_per_block(uint32_t T) {
+    const uint32_t want = (T + 1023) / 1024;              // about 1024 workgroups
+    const uint32_t r = (want + 15) / 16 * 16;
+    return r < 16 ? 16 : r > 128 ? 128 : r;
+}
+// Up to this many rows one workgroup routes alone, in one launch, without a workspace.
+constexpr uint32_t kRouteOneBlock = 32;
+inline uint32_t route_blocks(uint32_t T) {
+    if (T <= kRouteOneBlock) return 1;
+    const uint32_t r = route_rows_per_block(T);
+    return (T + r - 1) / r;
+}
+// Per workgroup: E counts, E sums of probabilities, and the number of live rows.
+inline size_t route_workspace_bytes(uint32_t T, uint32_t E) {
+    return T <= kRouteOneBlock ? 0 : (size_t)route_blocks(T) * (2 * (size_t)E + 1) * 4;
+}
+
 // Size of the library-owned split-K scratch of gemm_bf16_splitk_noalloc, per
 // device (noalloc.hip).
 constexpr size_t kNoallocScratchBytes = BG_NOALLOC_SCRATCH_BYTES;
@@ -85,5 +153,14 @@ hipError_t launch_splitk_reduce(const float* ws, uint16_t* C, uint32_t M, uint32
                                 uint32_t splits, hipStream_t stream);
 hipError_t launch_scaled_add(uint16_t* out, const uint16_t* delta, size_t count, float scale,
                              hipStream_t stream);
+
+hipError_t launch_mxfp4_quantize(const MxQuantProblem& p, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, void* out, int type, uint32_t M,
+                                   uint32_t K, hipStream_t stream);
+// Dense (offsets NULL) and grouped MXFP4 products; K > 0 or K == 0 (zeros).
+hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream);
+// T may be 0 (the sums of an empty batch are still written).
+hipError_t launch_moe_route(const RouteProblem& p, hipStream_t stream);
+hipError_t launch_moe_route_backward(const RouteBackwardProblem& p, hipStream_t stream);
 
 }  // namespace bg

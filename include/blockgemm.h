@@ -393,6 +393,160 @@ bg_status gemm_w4a16_t(const uint16_t* A, const uint8_t* Bt, const uint8_t* SFBt
                        uint16_t* C, uint32_t M, uint32_t N, uint32_t K, void* stream);
 
 /*
+ * Element types of the operands that come in two: BF16 (raw 16-bit patterns)
+ * or FP32.
+ */
+typedef enum bg_type { BG_BF16 = 0, BG_F32 = 1 } bg_type;
+
+/*
+ * MXFP4 (OCP Microscaling Formats v1.0): 32 consecutive elements of a row are
+ * a block. Element k of a row has the value e2m1(code k) * 2^(s - 127), s the
+ * block's E8M0 byte (255 = NaN: the whole block is NaN). Codes are packed two
+ * a byte as everywhere in this library (element 2t in the LOW nibble), in
+ * [rows, K/2] bytes; scales are plain [rows, K/32] bytes. K must be a multiple
+ * of 32 (BG_ERR_SHAPE otherwise).
+ *
+ * mxfp4_quantize: rows of BF16 or FP32 values -> MXFP4. Per block, with top =
+ * max |x|:
+ *   s = max(floor(log2(top)) - 2 + 127, 0)   (0 where top is zero or subnormal)
+ *   code k = e2m1 nearest to x[k] * 2^(127 - s), ties to the even code,
+ *            magnitudes above 6 to 6 (a block whose top lies in (6, 8) * 2^(s - 127)
+ *            saturates); the sign of a zero is kept.
+ * A block that holds a NaN or an infinity gets s = 255 and codes 0.
+ *
+ *  x:      [M, K] values of x_type; row i starts ldx elements after row i-1,
+ *          ldx >= K. Rows whose pitch is not a multiple of 16 bytes take a
+ *          slower element-wise load path.
+ *  rows:   NULL (then R == M, BG_ERR_SHAPE otherwise: row i of the result is
+ *          row i of x), or R int32 on the device: row i of the result is row
+ *          rows[i] of x, and all zero (codes 0, scales 0) where rows[i] is
+ *          not in 0 .. M-1. A row may be listed any number of times. 4-byte
+ *          aligned.
+ *  codes:  [R, K/2] bytes, scales: [R, K/32] bytes, written; must not overlap
+ *          x, rows or each other (BG_ERR_ALIAS).
+ */
+bg_status mxfp4_quantize(const void* x, int x_type, uint32_t ldx, const int32_t* rows, uint8_t* codes,
+                         uint8_t* scales, uint32_t M, uint32_t R, uint32_t K, void* stream);
+
+/*
+ * mxfp4_dequantize: the values of an MXFP4 operand, out[i,k] = e2m1 * 2^(s-127),
+ * as BF16 or FP32 (out_type). Every value is exact in both; magnitudes of
+ * 2^128 and more (s >= 252 only) become infinities.
+ *
+ *  codes: [M, K/2], scales: [M, K/32], read. out: [M, K], written, overlapping
+ *  neither (BG_ERR_ALIAS).
+ */
+bg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, void* out, int out_type, uint32_t M,
+                           uint32_t K, void* stream);
+
+/*
+ * gemm_mxfp4: C[i,j] = bf16( sum_k a[i,k] * b[j,k] ) for MXFP4 operands, FP32
+ * accumulation on the block-scaled FP4 matrix cores, which take the E2M1
+ * codes and the E8M0 scales as they are stored. The summation order is
+ * unspecified but fixed by the shape: repeated calls return identical bits.
+ *
+ *  A: [M, K/2], SFA: [M, K/32], B: [N, K/2], SFB: [N, K/32] bytes, read.
+ *  C: [M, N] BF16, written; must not overlap an input (BG_ERR_ALIAS).
+ */
+bg_status gemm_mxfp4(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB, uint16_t* C,
+                     uint32_t M, uint32_t N, uint32_t K, void* stream);
+
+/*
+ * gemm_mxfp4_grouped: the experts' products. Rows offsets[e] .. offsets[e+1]-1
+ * of A are multiplied with expert e's weights:
+ *   C[i,j] = bf16( sum_k a[i,k] * b[e,j,k] ).
+ *
+ *  A: [S, K/2], SFA: [S, K/32] bytes (rows sorted by expert).
+ *  B: [E, N, K/2], SFB: [E, N, K/32] bytes.
+ *  offsets: E + 1 int32 on the device, non-decreasing, 0 <= offsets <= S; an
+ *           expert may have no rows. They are read on the device only and
+ *           clamped to 0 .. S there, so that no other values can make the
+ *           call read or write out of bounds (what it computes then is
+ *           unspecified). 4-byte aligned.
+ *  C: [S, N] BF16. Rows before offsets[0] and from offsets[E] on are left as
+ *     they were. C must not overlap an input (BG_ERR_ALIAS).
+ *  E <= 1024 (BG_ERR_SHAPE otherwise). E == 0, S == 0 or N == 0: nothing to do.
+ */
+bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB,
+                             const int32_t* offsets, uint16_t* C, uint32_t S, uint32_t N, uint32_t K, uint32_t E,
+                             void* stream);
+
+/*
+ * moe_route: a router's decisions from its logits (gemm_bf16_ordered's BF16 or
+ * gemm_bf16_ordered_f32's FP32 output), with the balance loss of training and
+ * the dispatch order gemm_mxfp4_grouped takes.
+ *
+ * A row t is live where valid[t] != 0 (or valid is NULL) and it holds at least
+ * one logit above -infinity. For live rows p[t,e] = softmax over e, in FP32;
+ * with n live rows:
+ *   ids[t,j]      the k largest logits' experts, largest first, ties to the
+ *                 lowest index; -infinity and NaN are never chosen
+ *   weights[t,j]  p of the chosen, divided by their sum if normalize != 0
+ *   counts[e]     how often e was chosen
+ *   mean_probs[e] sum_t p[t,e] / n
+ *   loss          E / (k n) * sum_e counts[e] * mean_probs[e]   (1 when even)
+ *   offsets[e]    sum of counts before e (E + 1 of them)
+ *   rows[i]       the places 0 .. T*k-1 sorted by expert, then by row: the row
+ *                 at place i; -1 from offsets[E] on
+ *   pos[t,j]      the place of row t's j-th choice
+ *   n_valid       n
+ * Choices that do not exist (rows that are not live, or with fewer than k
+ * logits above -infinity) have ids -1, weights 0, pos -1. With n = 0, loss and
+ * mean_probs are 0. A live row with a NaN or a +infinity has NaN weights, and
+ * makes mean_probs and loss NaN; its ids and places stay valid. Logits of rows
+ * that valid leaves out are not read. Sums over rows are added in a fixed
+ * order: repeated calls return identical bits.
+ *
+ *  logits: [T, E] of logits_type, read.  valid: T bytes or NULL.
+ *  out:    a host struct of device pointers, all required where their array is
+ *          non-empty, overlapping neither each other nor an input or the
+ *          workspace (BG_ERR_ALIAS), 4-byte aligned.
+ *  workspace: device buffer of moe_route_workspace_bytes(T, E) bytes, 16-byte
+ *          aligned (BG_ERR_WORKSPACE if missing or smaller). It needs no
+ *          initialization; calls that may run concurrently need separate ones.
+ *  1 <= E <= 1024, 1 <= k <= min(E, 16), T * k < 2^31 (BG_ERR_SHAPE otherwise).
+ *  T == 0 writes counts, offsets, mean_probs, loss and n_valid (zeros).
+ */
+typedef struct bg_moe_routing {
+    int32_t* ids;        /* [T, k]  */
+    float* weights;      /* [T, k]  */
+    int32_t* counts;     /* [E]     */
+    int32_t* offsets;    /* [E + 1] */
+    int32_t* rows;       /* [T * k] */
+    int32_t* pos;        /* [T, k]  */
+    float* mean_probs;   /* [E]     */
+    float* loss;         /* [1]     */
+    int32_t* n_valid;    /* [1]     */
+} bg_moe_routing;
+
+bg_status moe_route(const void* logits, int logits_type, const uint8_t* valid, const bg_moe_routing* out,
+                    void* workspace, size_t workspace_bytes, uint32_t T, uint32_t E, uint32_t k, int normalize,
+                    void* stream);
+
+/* Bytes of workspace moe_route needs (0 where it needs none). */
+size_t moe_route_workspace_bytes(uint32_t T, uint32_t E);
+
+/*
+ * moe_route_backward: dlogits of moe_route, for the gradients dweights of its
+ * weights and dloss of its loss (ids, counts and places have none):
+ *   c[e] = dloss * E * counts[e] / (k n^2)
+ *   dlogits[t,e] = p[t,e] * (c[e] - sum_f p[t,f] c[f]) + the weights' part:
+ *     normalized:  w_j (dw_j - sum_i w_i dw_i) at the expert of choice j
+ *     plain:       w_j dw_j there, less p[t,e] * sum_i w_i dw_i everywhere
+ * and 0 for rows that are not live. ids, weights, counts and n_valid are
+ * moe_route's outputs for the same logits, k and normalize.
+ *
+ *  dweights: [T, k] FP32 or NULL (zero).  dloss: one FP32 on the device or NULL
+ *  (zero).  dlogits: [T, E] of logits_type, written; it may be the logits
+ *  themselves (each row is read before it is written), and must not overlap
+ *  any other input (BG_ERR_ALIAS).  Sizes as moe_route.
+ */
+bg_status moe_route_backward(const void* logits, int logits_type, const int32_t* ids, const float* weights,
+                             const int32_t* counts, const int32_t* n_valid, const float* dweights,
+                             const float* dloss, void* dlogits, uint32_t T, uint32_t E, uint32_t k, int normalize,
+                             void* stream);
+
+/*
  * bf16_scaled_add: out[i] = bf16( f32(out[i]) + fl32(scale * f32(delta[i])) )
  * over `count` BF16 elements. The second half of the unfused LoRA fold that
  * gemm_bf16_scaled_acc must equal bit for bit (gemm_dense.rs page, doc comment

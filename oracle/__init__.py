@@ -45,3 +45,12 @@ from .gemm import (  # noqa: F401
     splitk_reduce,
     tolerance,
 )
+from .mxfp4 import (  # noqa: F401, E402
+    dequant_mxfp4,
+    e8m0_to_f64,
+    f64_to_e2m1,
+    gemm_mxfp4_abs,
+    gemm_mxfp4_grouped_ref,
+    gemm_mxfp4_ref,
+    quantize_mxfp4,
+)
