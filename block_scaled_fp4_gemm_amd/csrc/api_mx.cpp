@@ -89,7 +89,7 @@ bg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, void* ou
 
 bg_status gemm_mxfp4(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB, uint16_t* C,
                      uint32_t M, uint32_t N, uint32_t K, void* stream) {
-    if (!dims_ok(M, N, K) || K % 32 != 0 || !fits(M, K, 1, 1) || !fits(N, K, 1, 1) || !fits(M, N, 1, 2))
+    if (!dims_ok(M, N, K) || K % 32 != 0 || K > kMaxMxK || !fits(M, K, 1, 1) || !fits(N, K, 1, 1) || !fits(M, N, 1, 2))
         return BG_ERR_SHAPE;
     if (M == 0 || N == 0) return BG_OK;
     bg_status s = check_mx_gemm(A, SFA, B, SFB, nullptr, C, M, N, K, 1);
@@ -103,7 +103,7 @@ bg_status gemm_mxfp4(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, con
 bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB,
                              const int32_t* offsets, uint16_t* C, uint32_t S, uint32_t N, uint32_t K, uint32_t E,
                              void* stream) {
-    if (!dims_ok(S, N, K) || K % 32 != 0 || E > kMaxExperts || !fits(N, K, E, 1) || !fits(S, K, 1, 1) ||
+    if (!dims_ok(S, N, K) || K % 32 != 0 || K > kMaxMxK || E > kMaxExperts || !fits(N, K, E, 1) || !fits(S, K, 1, 1) ||
         !fits(S, N, 1, 2))
         return BG_ERR_SHAPE;
     if (S == 0 || N == 0 || E == 0) return BG_OK;

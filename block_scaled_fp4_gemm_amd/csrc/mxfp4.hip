@@ -3,6 +3,8 @@
 //
 // Format (OCP Microscaling Formats v1.0): 32 consecutive K elements share one
 // E8M0 scale byte s, element = e2m1(code) * 2^(s - 127), s = 255 is NaN.
+#include <type_traits>
+
 #include "bg_internal.hpp"
 #include "tile_order.hpp"
 
@@ -13,6 +15,10 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// the same at any address: global memory takes unaligned accesses
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -182,53 +188,607 @@ __device__ __forceinline__ TileRows group_tile(const int32_t* offsets, int E, in
     return TileRows{0, 0, 0};
 }
 
-// The plain form of the product: one wave per 32 x 32 tile, operands straight
-// from memory. Lane l of the instruction holds 32 consecutive K elements (one
-// block, 16 bytes, and its scale byte) of row l % 32, blocks 2t and 2t + 1 in
-// the two halves of the wave.
-__global__ void __launch_bounds__(256)
-mx_gemm_kernel(MxGemmProblem p, int tiles_n) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
-    TileRows t{0, tm * 32, min(32, (int)p.M - tm * 32)};
-    if (p.offsets != nullptr) t = group_tile(p.offsets, (int)p.E, (int)p.M, 32, tm, lane);
-    if (t.rows <= 0) return;
-    const int n0 = tn * 128 + wave * 32;
-    if (n0 >= (int)p.N) return;
-    const int blocks = (int)(p.K / 32);
-    const int64_t ra = t.row0 + min(lane & 31, t.rows - 1);
-    const int64_t rb = (int64_t)t.e * p.N + min(n0 + (lane & 31), (int)p.N - 1);
-    const uint8_t *a = p.A + ra * (p.K / 2), *b = p.B + rb * (p.K / 2);
-    const uint8_t *sa = p.SFA + ra * blocks, *sb = p.SFB + rb * blocks;
-    f32x16 acc = {};
-    for (int c = lane >> 5; c - (lane >> 5) < blocks; c += 2) {
-        u32x4 wa = {}, wb = {};
-        int ea = 127, eb = 127;
-        if (c < blocks) {
-            wa = *reinterpret_cast<const u32x4*>(a + (int64_t)c * 16);
-            wb = *reinterpret_cast<const u32x4*>(b + (int64_t)c * 16);
-            ea = sa[c];
-            eb = sb[c];
-        }
-        const i32x8 fa = {(int)wa.x, (int)wa.y, (int)wa.z, (int)wa.w, 0, 0, 0, 0};
-        const i32x8 fb = {(int)wb.x, (int)wb.y, (int)wb.z, (int)wb.w, 0, 0, 0, 0};
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb, fa, acc, 4, 4, 0, eb, 0, ea);
-    }
-    const int m = lane & 31;
-    if (m >= t.rows) return;
-    uint16_t* out = p.C + (int64_t)(t.row0 + m) * p.N;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int n = n0 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        if (n < (int)p.N) out[n] = (uint16_t)pack_bf16x2(acc[v], 0.0f);
-    }
-}
-
 // Workgroups of a kernel that loops over the rest (a launch holds fewer than 2^32 threads).
 uint32_t grid_of(uint64_t groups) { return (uint32_t)(groups < (1u << 20) ? groups : (1u << 20)); }
 
-// A grid of one workgroup of 256 threads per tile.
-bool tiles_fit(uint64_t tiles) { return tiles < (1u << 24); }
+// A grid of one workgroup of at most 512 threads per tile.
+bool tiles_fit(uint64_t tiles) { return tiles < (1u << 23); }
+
+// Compile-time loops over a constant's values.
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (N > 0) {
+        static_for<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    static_assert(N >= 0 && N <= 63, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A barrier that orders LDS only: a full fence would also wait for the direct
+// loads in flight, which are counted by hand.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A pointer every lane holds the same value of, in scalar registers.
+__device__ __forceinline__ void* uniform_ptr(const void* p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    return reinterpret_cast<void*>(((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) const uint8_t*)p);
+}
+
+// Scheduling of one part of a step: NM matrix instructions, each followed by
+// an LDS read while the NR reads last.
+template <int NM, int NR>
+__device__ __forceinline__ void interleave() {
+    constexpr int R = (NR + NM - 1) / NM;
+#pragma unroll
+    for (int q = 0; q < NM; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (q * R < NR) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+}
+
+constexpr int STEP = 8;                         // blocks per K step: 128 bytes of every row, one cache line
+constexpr int PAIR = 2 * STEP;                  // scales are staged for two steps at once: 16 bytes of every row
+
+// Swizzled 16-byte slot of block c in row `row` of a staged tile of eight
+// blocks a row: the rows that the lanes of one 16-byte LDS read touch spread
+// over all banks. An involution in c.
+__device__ __forceinline__ int block_slot(int row, int c) { return c ^ ((row ^ (row >> 3)) & 7); }
+
+// Direct global -> LDS staging of ROWS rows' codes, 128 bytes a row and step,
+// shared out over NW waves. One instruction moves 64 x 16 bytes, eight rows,
+// into one contiguous KB of LDS. Rows past the last are clamped to it. Where a
+// wave has a surplus instruction it loads the last stretch again, so every
+// wave issues the same number.
+// The loads are inline assembly: the compiler's wait insertion cannot tell the
+// stages apart and would wait for them at every LDS read. Their completion is
+// tracked with s_waitcnt vmcnt before the barrier that precedes their first use.
+template <int ROWS, int NW>
+struct MxStager {
+    static constexpr int SEGS = ROWS / 8, PER = (SEGS + NW - 1) / NW;
+    uint32_t off[PER];   // byte offsets from the tile's first row at step 0
+    __amdgpu_buffer_rsrc_t rsrc;
+
+    __device__ __forceinline__ static int seg(int wave, int j) { return min(wave + j * NW, SEGS - 1); }
+    // the block a lane fetches of its row: it lands in slot lane % 8
+    __device__ __forceinline__ static int block(int wave, int j, int lane) {
+        return block_slot(seg(wave, j) * 8 + lane / 8, lane % 8);
+    }
+
+    // data: the tile's first row; last: the last row that exists, from there on
+    __device__ __forceinline__ void init(const uint8_t* data, int last, uint32_t blocks, int wave, int lane) {
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(data), (short)0, 0xFFFFFFFF, 0x00020000);
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            off[j] = (uint32_t)min(seg(wave, j) * 8 + lane / 8, last) * (blocks * 16) +
+                     (uint32_t)block(wave, j, lane) * 16;
+    }
+
+    // Before the last step, if only `left` blocks remain there: lanes whose
+    // block lies past the row's end fetch its last one.
+    __device__ __forceinline__ void clamp_to(int left, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) off[j] -= (uint32_t)max(block(wave, j, lane) - (left - 1), 0) * 16;
+    }
+
+    // the codes of the step that starts at block c0
+    __device__ __forceinline__ void issue(uint32_t c0, uint8_t* lds, int wave) const {
+        const uint32_t s = c0 * 16;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off[j]), "s"(rsrc), "s"(s),
+                         "{m0}"(lds_addr(lds) + seg(wave, j) * 1024));
+    }
+
+    // codes past the rows' end become zeros (each wave those it fetched itself)
+    __device__ __forceinline__ void zero_past(int left, uint8_t* lds, int wave, int lane) const {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (block(wave, j, lane) >= left)
+                *reinterpret_cast<u32x4*>(lds + seg(wave, j) * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+    }
+};
+
+// Scales of the BM rows of A and the BN rows of B of a tile, as [row][16] bytes
+// of a pair of steps in LDS. FULL (rows of whole steps, at least two): direct
+// loads of 16 bytes a row, one row a lane. A row of 8 bytes a step costs a
+// cache request for every 8 bytes, as many as all its codes; two steps at once
+// halve that (64 x 64 tiles, 128 x 7168 x 16384: 27 us before, 22 us after). A
+// last pair that holds only one step starts a step early, so that nothing is
+// read past a row. Otherwise in words of any alignment through registers, a
+// step at a time, scale 0 past the row's end.
+template <int BM, int BN, int NW, bool FULL>
+struct ScaleStager {
+    static constexpr int SEGS = (BM + BN) / 64, PER = FULL ? (SEGS + NW - 1) / NW : 0;
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "a stretch belongs to one operand");
+    static constexpr int WORDS = (BM + BN) * 2, WPER = (WORDS + NW * 64 - 1) / (NW * 64);
+    uint32_t off[FULL ? PER : WPER];
+    uint32_t reg[FULL ? 1 : WPER];
+    __amdgpu_buffer_rsrc_t rsrc[FULL ? PER : 1];
+    const uint8_t *sa, *sb;
+
+    __device__ __forceinline__ static int seg(int wave, int j) { return min(wave + j * NW, SEGS - 1); }
+
+    __device__ __forceinline__ void init(const uint8_t* a, const uint8_t* b, int last_a, int last_b, uint32_t blocks,
+                                         int wave, int lane) {
+        if constexpr (FULL) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int r = seg(wave, j) * 64;
+                const bool is_a = r < BM;
+                rsrc[j] = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(is_a ? a : b), (short)0, 0xFFFFFFFF, 0x00020000);
+                off[j] = (uint32_t)(is_a ? min(r + lane, last_a) : min(r - BM + lane, last_b)) * blocks;
+            }
+        } else {
+            sa = a;
+            sb = b;
+#pragma unroll
+            for (int j = 0; j < WPER; ++j) {
+                const int r = min((j * NW + wave) * 64 + lane, WORDS - 1) / 2;
+                off[j] = (uint32_t)(r < BM ? min(r, last_a) : min(r - BM, last_b)) * blocks;
+            }
+        }
+    }
+    // first block of the pair that a step's scales are staged with
+    __device__ __forceinline__ static uint32_t pair_start(int step, uint32_t blocks) {
+        const uint32_t c = (uint32_t)(step / 2) * PAIR;
+        return FULL ? min(c, blocks - PAIR) : c;
+    }
+    __device__ __forceinline__ void issue(uint32_t c0, uint8_t* lds, int wave) const {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off[j]), "s"(rsrc[j]), "s"(c0),
+                         "{m0}"(lds_addr(lds) + seg(wave, j) * 1024));
+    }
+    __device__ __forceinline__ void fetch(int step, uint32_t blocks, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < WPER; ++j) {
+            const int w = min((j * NW + wave) * 64 + lane, WORDS - 1);
+            const uint8_t* q = (w / 2 < BM ? sa : sb) + off[j];
+            const uint32_t c = (uint32_t)(step * STEP + (w & 1) * 4);
+            if (blocks >= 4) {
+                const uint32_t at = min(c, blocks - 4), past = c - at;      // the row's last word, shifted down
+                reg[j] = past < 4 ? *reinterpret_cast<const u32_any*>(q + at) >> (8 * past) : 0u;
+            } else {
+                reg[j] = 0;
+                for (uint32_t b = c; b < min(c + 4, blocks); ++b) reg[j] |= (uint32_t)q[b] << (8 * (b - c));
+            }
+        }
+    }
+    __device__ __forceinline__ void store(int step, uint8_t* lds, int wave, int lane) const {
+#pragma unroll
+        for (int j = 0; j < WPER; ++j) {
+            const int w = min((j * NW + wave) * 64 + lane, WORDS - 1);
+            *reinterpret_cast<uint32_t*>(lds + (w / 2) * 16 + (step & 1) * STEP + (w & 1) * 4) = reg[j];
+        }
+    }
+};
+
+// Tile kernel. A workgroup of WM x WN waves owns a BM x BN tile of C and walks
+// K in steps of 256 elements, four matrix instructions deep: lane l of
+// instruction s holds block 4 (l / 32) + s of row l % 32 (the order of K inside
+// a product is free as long as A and B agree), so the four scale bytes a lane
+// needs for a step are one aligned word, and the instruction picks byte s of
+// it: no vector instruction touches codes or scales between LDS and the matrix
+// cores. The steps' codes go through a ring of STAGES buffers in LDS, the
+// scales through buffers of a pair of steps, filled by direct loads.
+// FULL: K is whole steps, two at least. Otherwise the last step is finished by
+// zeroing A's blocks past the end after they landed (their scales and B's are
+// not NaN: zero, or another block's of B).
+// The matrix instruction takes B first, so a lane ends up with four
+// consecutive columns of one row of C.
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool FULL>
+__global__ void __launch_bounds__(WM * WN * 64)
+mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
+    constexpr int NW = WM * WN;
+    constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+    static_assert(FM * 32 * WM == BM && FN * 32 * WN == BN, "whole instructions per wave");
+    // A pair of scales is loaded with the codes of its first step, STAGES steps
+    // ahead, and read last one step after it: so many pairs are there at once.
+    constexpr int PAIRS = STAGES / 2 + 1;
+    constexpr int STAGE = (BM + BN) * 128, SCALES = (BM + BN) * PAIR;
+    constexpr int RING = STAGES * STAGE + PAIRS * SCALES, OUT = BM * BN * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > OUT ? RING : OUT];
+    uint8_t* const scale_mem = smem + STAGES * STAGE;
+    using StA = MxStager<BM, NW>;
+    using StB = MxStager<BN, NW>;
+    using StS = ScaleStager<BM, BN, NW, FULL>;
+    // loads a wave has in flight, at least, when only those of the STAGES - 1
+    // or STAGES - 2 youngest steps are
+    constexpr int L = StA::PER + StB::PER;
+    constexpr int AHEAD1 = (STAGES - 1) * L + (STAGES - 1) / 2 * StS::PER;
+    constexpr int AHEAD2 = (STAGES - 2) * L + (STAGES - 2) / 2 * StS::PER;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    int tm, tn;
+    TileRows t;
+    if constexpr (GROUPED) {
+        // the tiles of one row of tiles share an XCD (its rows of A, and with
+        // them the expert, stay in one L2); rows of tiles are dealt out to the
+        // XCDs in turn, so the ones that do not exist are spread evenly
+        const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
+        tm = (j / tiles_n) * 8 + x;
+        tn = j % tiles_n;
+        t = group_tile(p.offsets, (int)p.E, (int)p.M, BM, tm, lane);
+        t.e = __builtin_amdgcn_readfirstlane(t.e);
+        t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+        if (t.rows <= 0) return;
+    } else {
+        tile_of<ORDER_GEMM>((int)blockIdx.x, tiles_m, tiles_n, tm, tn);
+        t = TileRows{0, tm * BM, min(BM, (int)p.M - tm * BM)};
+    }
+    const int n0 = tn * BN;
+    const uint32_t blocks = p.K / 32;
+    const int nsteps = (int)((blocks + STEP - 1) / STEP);
+    const bool ragged = !FULL && blocks % STEP != 0;
+    const int64_t rb = (int64_t)t.e * p.N + n0;
+    const int last_a = t.rows - 1, last_b = min(BN, (int)p.N - n0) - 1;
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+
+    if (nsteps > 0) {
+        StA sa;
+        StB sb;
+        StS ss;
+        sa.init(p.A + (int64_t)t.row0 * blocks * 16, last_a, blocks, wave, lane);
+        sb.init(p.B + rb * blocks * 16, last_b, blocks, wave, lane);
+        ss.init(p.SFA + (int64_t)t.row0 * blocks, p.SFB + rb * blocks, last_a, last_b, blocks, wave, lane);
+
+        // a stage: A's codes, B's codes; before those of an even step, its pair of scales
+        auto pair_mem = [&](int step) { return scale_mem + (uint32_t)(step / 2) % PAIRS * SCALES; };
+        auto issue = [&](int step, uint8_t* st) {
+            const int s = min(step, nsteps - 1);       // past the end: the last one again
+            if constexpr (FULL)
+                if ((step & 1) == 0) ss.issue(StS::pair_start(s, blocks), pair_mem(step), wave);
+            sa.issue((uint32_t)s * STEP, st, wave);
+            sb.issue((uint32_t)s * STEP, st + BM * 128, wave);
+        };
+        auto fetch = [&](int step) {
+            if constexpr (!FULL) ss.fetch(step, blocks, wave, lane);
+        };
+        auto store = [&](int step) {
+            if constexpr (!FULL) ss.store(step, pair_mem(step), wave, lane);
+        };
+        auto clamp = [&](int step) {           // before the first issue of the last step
+            if (ragged && step == nsteps - 1) {
+                sa.clamp_to((int)(blocks % STEP), wave, lane);
+                sb.clamp_to((int)(blocks % STEP), wave, lane);
+            }
+        };
+        auto zero = [&](int step, uint8_t* st) {   // after the last step has landed
+            if (ragged && step == nsteps - 1) sa.zero_past((int)(blocks % STEP), st, wave, lane);
+        };
+
+        // Fragment addresses: block 4h + s of row 32 i + l % 32 of the wave's
+        // rows; every second fragment's swizzle differs in bit 2 (64 bytes).
+        const int row = lane & 31, h = lane >> 5;
+        uint32_t va[4], vb[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            va[s] = (uint32_t)((wm * TM + row) * 128 + block_slot(wm * TM + row, 4 * h + s) * 16);
+            vb[s] = (uint32_t)((BM + wn * TN + row) * 128 + block_slot(wn * TN + row, 4 * h + s) * 16);
+        }
+        const uint32_t vsa = (uint32_t)((wm * TM + row) * PAIR + h * 4), vsb = (uint32_t)((BM + wn * TN + row) * PAIR + h * 4);
+        auto frags = [&](const uint8_t* st, int s, u32x4 (&a)[FM], u32x4 (&b)[FN]) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                a[i] = *reinterpret_cast<const u32x4*>(st + (va[s] ^ (64u * (i & 1))) + 4096 * i);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                b[j] = *reinterpret_cast<const u32x4*>(st + (vb[s] ^ (64u * (j & 1))) + 4096 * j);
+        };
+        auto exps = [&](int step, int (&a)[FM], int (&b)[FN]) {
+            const uint8_t* q = pair_mem(step) + ((uint32_t)step * STEP - StS::pair_start(step, blocks));
+#pragma unroll
+            for (int i = 0; i < FM; ++i) a[i] = *reinterpret_cast<const int*>(q + vsa + 32 * PAIR * i);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) b[j] = *reinterpret_cast<const int*>(q + vsb + 32 * PAIR * j);
+        };
+        auto mfma = [&](auto sc, const u32x4 (&a)[FM], const u32x4 (&b)[FN], const int (&xa)[FM], const int (&xb)[FN]) {
+            constexpr int s = decltype(sc)::value;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const i32x8 A = {(int)a[i].x, (int)a[i].y, (int)a[i].z, (int)a[i].w, 0, 0, 0, 0};
+                    const i32x8 B = {(int)b[j].x, (int)b[j].y, (int)b[j].z, (int)b[j].w, 0, 0, 0, 0};
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(B, A, acc[i][j], 4, 4, s, xb[j], s, xa[i]);
+                }
+        };
+
+        fetch(0);
+        clamp(0);
+        issue(0, smem);
+        store(0);
+#pragma unroll
+        for (int st = 1; st < STAGES; ++st) {
+            clamp(st);
+            issue(st, smem + st * STAGE);
+        }
+        wait_vmcnt<AHEAD1>();
+        zero(0, smem);
+        lds_barrier();
+        fetch(1);
+
+        // the next step's stage, landed for every wave; this step's is free and refilled
+        int cur = 0;
+        auto advance = [&](int k) {
+            uint8_t* st = smem + cur * STAGE;
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            uint8_t* sn = smem + cur * STAGE;
+            wait_vmcnt<AHEAD2>();                  // step k + 1 has landed for this wave ...
+            store(k + 1);
+            zero(k + 1, sn);
+            clamp(k + STAGES);
+            lds_barrier();                         // ... and for all, and all have read step k
+            __builtin_amdgcn_sched_barrier(0);
+            issue(k + STAGES, st);
+            fetch(k + 2);
+            return sn;
+        };
+        if constexpr (FM * FN <= 4) {
+            // Small wave tiles: an instruction's worth of products is shorter
+            // than an LDS read takes, so a whole step's fragments are read
+            // while the step before is multiplied (64 x 64 tile, 64 rows, N
+            // 4096, K 7168: 10.5 us reading one instruction ahead).
+            u32x4 fa[2][4][FM], fb[2][4][FN];
+            int ea[2][FM], eb[2][FN];
+            auto read = [&](int k, const uint8_t* st, auto q) {
+                constexpr int Q = decltype(q)::value;
+                exps(k, ea[Q], eb[Q]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) frags(st, s, fa[Q][s], fb[Q][s]);
+            };
+            auto multiply = [&](auto q) {
+                constexpr int Q = decltype(q)::value;
+                static_for<4>([&](auto s) { mfma(s, fa[Q][decltype(s)::value], fb[Q][decltype(s)::value], ea[Q], eb[Q]); });
+            };
+            constexpr std::integral_constant<int, 0> EVEN{};
+            constexpr std::integral_constant<int, 1> ODD{};
+            read(0, smem, EVEN);
+            auto step = [&](int k, auto q, auto other) {
+                const uint8_t* sn = advance(k);
+                read(k + 1, sn, other);
+                multiply(q);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            int k = 0;
+            for (; k + 2 < nsteps; k += 2) {
+                step(k, EVEN, ODD);
+                step(k + 1, ODD, EVEN);
+            }
+            if (k + 1 < nsteps) {
+                step(k, EVEN, ODD);
+                multiply(ODD);
+            } else {
+                multiply(EVEN);
+            }
+        } else {
+            // Instruction s of a step multiplies what was read during s - 1.
+            // The barrier that retires a step comes before its last
+            // instructions, whose operands are in registers, so the matrix
+            // cores have work while the freed stage is refilled and the next
+            // one's first fragments are read.
+            u32x4 fa[2][FM], fb[2][FN];
+            int ea[FM], eb[FN];
+            frags(smem, 0, fa[0], fb[0]);
+            exps(0, ea, eb);
+            auto leading = [&](const uint8_t* st) {
+                static_for<3>([&](auto s) {
+                    constexpr int S = decltype(s)::value;
+                    frags(st, S + 1, fa[(S + 1) & 1], fb[(S + 1) & 1]);
+                    mfma(s, fa[S & 1], fb[S & 1], ea, eb);
+                    interleave<FM * FN, FM + FN>();
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            };
+            for (int k = 0; k + 1 < nsteps; ++k) {
+                leading(smem + cur * STAGE);
+                const uint8_t* sn = advance(k);
+                int xa[FM], xb[FN];
+                frags(sn, 0, fa[0], fb[0]);
+                exps(k + 1, xa, xb);
+                mfma(std::integral_constant<int, 3>{}, fa[1], fb[1], ea, eb);
+                interleave<FM * FN, 2 * (FM + FN)>();
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) ea[i] = xa[i];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) eb[j] = xb[j];
+            }
+            leading(smem + cur * STAGE);
+            mfma(std::integral_constant<int, 3>{}, fa[1], fb[1], ea, eb);
+        }
+        wait_vmcnt<0>();       // what was loaded past the end lands before LDS is used again
+    }
+
+    // Epilogue: each wave turns its own part of the tile through LDS, so that
+    // rows leave in 16-byte pieces. Pieces rotate by row over the row's slots.
+    lds_barrier();
+    constexpr int OUTB = TN * 2, SLOTS = OUTB / 16;
+    uint8_t* mine = smem + wave * (TM * OUTB);
+    auto slot = [](int row, int c) { return row * OUTB + ((c + row) % SLOTS) * 16; };
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int r = i * 32 + (lane & 31), n = j * 32 + g * 8 + (lane >> 5) * 4;
+                *reinterpret_cast<u32x2*>(mine + slot(r, n >> 3) + (lane >> 5) * 8) =
+                    u32x2{pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                          pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
+            }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const bool vec = p.N % 8 == 0;
+    constexpr int RPI = 64 / SLOTS;            // rows per store instruction
+#pragma unroll 4
+    for (int r0 = 0; r0 < TM; r0 += RPI) {
+        const int r = r0 + lane / SLOTS, c = lane % SLOTS;
+        const int m = wm * TM + r, n = n0 + wn * TN + c * 8;
+        if (m >= t.rows || n >= (int)p.N) continue;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(mine + slot(r, c));
+        uint16_t* out = p.C + (int64_t)(t.row0 + m) * p.N + n;
+        if (n + 8 <= (int)p.N) {
+            if (vec)
+                __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(out));
+            else
+                *reinterpret_cast<u32x4_any*>(out) = w;
+        } else {
+            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+            for (int e = 0; e < 8 && n + e < (int)p.N; ++e) out[e] = (uint16_t)(w4[e >> 1] >> ((e & 1) * 16));
+        }
+    }
+}
+
+// Few rows: the weights' bytes are the time, so they go straight from memory
+// into the registers of the one wave that multiplies them, and enough of them
+// are in flight at once. A workgroup owns 16 columns and up to 16 MT rows; its
+// NW waves take K in turns of 512 elements (16 blocks), and the sums meet in
+// LDS, added in the waves' order. The matrix instruction is 16 x 16 x 128: lane
+// l of instruction s of a turn holds block 4s + l / 16 of row l % 16, so a load
+// of the wave covers 64 consecutive bytes of 16 rows, and its scale is byte
+// l / 16 of word s of the row's 16 scale bytes of the turn.
+template <int MT, int NW, bool GROUPED>
+__global__ void __launch_bounds__(NW * 64)
+mx_skinny_kernel(MxGemmProblem p, int tiles_n) {
+    constexpr int TURN = 16;                       // blocks per turn
+    __shared__ f32x4 part[NW][MT][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
+    TileRows t{0, tm * 16 * MT, min(16 * MT, (int)p.M - tm * 16 * MT)};
+    if constexpr (GROUPED) {
+        t = group_tile(p.offsets, (int)p.E, (int)p.M, 16 * MT, tm, lane);
+        if (t.rows <= 0) return;
+    }
+    const int n0 = tn * 16, r = lane & 15, g = lane >> 4;
+    const uint32_t blocks = p.K / 32;
+    const int64_t rb = (int64_t)t.e * p.N + min(n0 + r, (int)p.N - 1);
+    const uint8_t *b = p.B + rb * blocks * 16, *sb = p.SFB + rb * blocks;
+    const uint8_t *a[MT], *sa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t ra = t.row0 + min(16 * i + r, t.rows - 1);
+        a[i] = p.A + ra * blocks * 16;
+        sa[i] = p.SFA + ra * blocks;
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
+    auto mfma = [&](const u32x4& x, const u32x4& y, int ex, int ey, f32x4& c) {
+        const i32x8 X = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+        const i32x8 Y = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(Y, X, c, 4, 4, 0, ey, 0, ex);
+    };
+    // whole turns, the next one's loads in flight during a turn's products
+    u32x4 wb[2][4], wa[2][MT][4], eb[2], ea[2][MT];
+    auto load = [&](uint32_t c0, int q) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) wb[q][s] = *reinterpret_cast<const u32x4*>(b + (uint64_t)(c0 + 4 * s + g) * 16);
+        eb[q] = *reinterpret_cast<const u32x4_any*>(sb + c0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                wa[q][i][s] = *reinterpret_cast<const u32x4*>(a[i] + (uint64_t)(c0 + 4 * s + g) * 16);
+            ea[q][i] = *reinterpret_cast<const u32x4_any*>(sa[i] + c0);
+        }
+    };
+    auto multiply = [&](int q) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                mfma(wa[q][i][s], wb[q][s], (int)(ea[q][i][s] >> (8 * g)), (int)(eb[q][s] >> (8 * g)), acc[i]);
+    };
+    const uint32_t turns = blocks / TURN;
+    uint32_t u = wave;
+    if (u < turns) load(u * TURN, 0);
+    for (; u + NW < turns; u += 2 * NW) {
+        load((u + NW) * TURN, 1);
+        multiply(0);
+        if (u + 2 * NW < turns) load((u + 2 * NW) * TURN, 0);
+        multiply(1);
+    }
+    if (u < turns) multiply(0);
+    // the rest of K, by the next wave in turn: A's blocks past the end are zero
+    if (blocks % TURN != 0 && wave == (int)(turns % NW)) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t c = turns * TURN + 4 * s + g, cc = min(c, blocks - 1);
+            const u32x4 y = *reinterpret_cast<const u32x4*>(b + (uint64_t)cc * 16);
+            const int ey = sb[cc];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                u32x4 x = *reinterpret_cast<const u32x4*>(a[i] + (uint64_t)cc * 16);
+                if (c >= blocks) x = u32x4{0u, 0u, 0u, 0u};
+                mfma(x, y, sa[i][cc], ey, acc[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    // lane l of a 16 x 16 result holds columns 4 (l / 16) .. + 3 of row l % 16
+    for (int q = threadIdx.x; q < MT * 64; q += NW * 64) {
+        const int i = q >> 6, l = q & 63;
+        f32x4 c = part[0][i][l];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) c += part[w][i][l];
+        const int m = 16 * i + (l & 15), n = n0 + 4 * (l >> 4);
+        if (m >= t.rows) continue;
+        uint16_t* out = p.C + (int64_t)(t.row0 + m) * p.N + n;
+        const u32x2 w = {pack_bf16x2(c.x, c.y), pack_bf16x2(c.z, c.w)};
+        if (n + 4 <= (int)p.N)
+            *reinterpret_cast<u32x2_any*>(out) = w;
+        else
+            for (int e = 0; n + e < (int)p.N; ++e) out[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
+    }
+}
+
+template <int MT, int NW>
+hipError_t launch_skinny(const MxGemmProblem& p, hipStream_t stream) {
+    const uint64_t tiles_n = (p.N + 15) / 16;
+    const uint64_t tiles_m = p.offsets != nullptr ? p.M / (16 * MT) + (p.E < p.M ? p.E : p.M) : (p.M + 16 * MT - 1) / (16 * MT);
+    if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
+    auto k = p.offsets != nullptr ? mx_skinny_kernel<MT, NW, true> : mx_skinny_kernel<MT, NW, false>;
+    k<<<dim3((uint32_t)(tiles_m * tiles_n)), NW * 64, 0, stream>>>(p, (int)tiles_n);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES>
+hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
+    const uint64_t tiles_n = (p.N + BN - 1) / BN;
+    // every expert may end in a partly filled tile
+    uint64_t tiles_m = p.offsets != nullptr ? p.M / BM + (p.E < p.M ? p.E : p.M) : (p.M + BM - 1) / BM;
+    if (p.offsets != nullptr) tiles_m = (tiles_m + 7) / 8 * 8;      // whole turns over the XCDs
+    if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
+    const bool full = p.K % (STEP * 32) == 0 && p.K >= PAIR * 32;
+    auto k = p.offsets != nullptr ? (full ? mx_tile_kernel<BM, BN, WM, WN, STAGES, true, true>
+                                           : mx_tile_kernel<BM, BN, WM, WN, STAGES, true, false>)
+                                  : (full ? mx_tile_kernel<BM, BN, WM, WN, STAGES, false, true>
+                                           : mx_tile_kernel<BM, BN, WM, WN, STAGES, false, false>);
+    k<<<dim3((uint32_t)(tiles_m * tiles_n)), WM * WN * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+    return hipGetLastError();
+}
 
 }  // namespace
 
@@ -256,12 +816,51 @@ hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
 }
 
 hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
-    const int tiles_n = (int)((p.N + 127) / 128);
-    // every expert may end in a partly filled tile
-    const uint64_t tiles_m = p.offsets != nullptr ? p.M / 32 + (p.E < p.M ? p.E : p.M) : (p.M + 31) / 32;
-    if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
-    mx_gemm_kernel<<<dim3((uint32_t)(tiles_m * tiles_n)), 256, 0, stream>>>(p, tiles_n);
-    return hipGetLastError();
+    const uint32_t turns = (p.K + 511) / 512;
+    if (p.offsets != nullptr) {
+        // by the rows an expert has on average
+        const uint64_t mean = p.M / p.E;
+        if (mean <= 8) return turns >= 8 ? launch_skinny<1, 8>(p, stream) : launch_skinny<1, 4>(p, stream);
+        if (mean <= 48) return launch_tile<64, 64, 2, 2, 4>(p, stream);
+        return launch_tile<128, 128, 4, 2, 2>(p, stream);
+    }
+    // Up to 16 rows, and up to 32 where the 64-column tiles would be few:
+    // 1 x 4096 x 7168 5.0 us against 9.7 us with the smallest tile, 16 x 4096 x
+    // 7168 6.3 / 9.7 us, 32 x 4096 x 7168 8.4 / 9.8 us (32 x 12288 x 2048: 9.5 / 5.4 us).
+    if (p.M <= 16) return turns >= 8 ? launch_skinny<1, 8>(p, stream) : launch_skinny<1, 4>(p, stream);
+    if (p.M <= 32 && (uint64_t)p.N * 3 < (uint64_t)p.cus * 64) return launch_skinny<2, 4>(p, stream);
+    // The tile whose time, counted in rounds over the compute units, is least:
+    // us per tile and per step of 256 K elements, alone on a compute unit and
+    // as one of two (fitted to 20 shapes, 64 x 4096 x 7168 to 4096 x 4096 x 8192).
+    struct Tile {
+        int bm, bn;
+        double fixed, alone, paired;   // paired 0: one workgroup fills a compute unit's LDS
+    };
+    static constexpr Tile tiles[] = {{256, 256, 4.0, 2.15, 0}, {256, 128, 2.1, 1.19, 0}, {128, 128, 2.0, 0.68, 1.3},
+                                     {128, 64, 2.5, 0.45, 0.77}, {64, 64, 1.5, 0.31, 0.54}};
+    const double steps = (p.K + 255) / 256;
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < 5; ++i) {
+        const Tile& c = tiles[i];
+        const uint64_t n = (uint64_t)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn), cu = p.cus;
+        double t;
+        if (c.paired == 0) {
+            t = (double)((n + cu - 1) / cu) * (c.fixed + steps * c.alone);
+        } else {
+            const uint64_t rest = n % (2 * cu);
+            t = (double)(n / (2 * cu)) * (c.fixed + steps * c.paired);
+            if (rest != 0) t += c.fixed + steps * (rest <= cu ? c.alone : c.paired);
+        }
+        if (i == 0 || t < least) best = i, least = t;
+    }
+    switch (best) {
+        case 0: return launch_tile<256, 256, 2, 4, 2>(p, stream);
+        case 1: return launch_tile<256, 128, 4, 2, 2>(p, stream);
+        case 2: return launch_tile<128, 128, 4, 2, 2>(p, stream);
+        case 3: return launch_tile<128, 64, 2, 2, 3>(p, stream);
+    }
+    return launch_tile<64, 64, 2, 2, 4>(p, stream);
 }
 
 }  // namespace bg
