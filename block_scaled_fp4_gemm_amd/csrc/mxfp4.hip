@@ -152,11 +152,13 @@ struct TileRows {
     int e, row0, rows;
 };
 
-// Tile `tile` of the experts' row ranges cut into tiles of tm rows, expert by
-// expert. Every lane of the wave takes part and gets the same answer. The
+// The experts' row ranges cut into tiles of tm rows, expert by expert; the
+// tile of this workgroup's turn j on XCD x. Every XCD takes one contiguous
+// stretch of the tiles that exist, so the tiles of an expert meet its weights
+// in one L2. Every lane of the wave takes part and gets the same answer. The
 // offsets are clamped to 0 .. S and an end before its start counts as empty,
 // so no offsets lead outside the operands.
-__device__ __forceinline__ TileRows group_tile(const int32_t* offsets, int E, int S, int tm, int tile, int lane) {
+__device__ __forceinline__ TileRows group_tile(const int32_t* offsets, int E, int S, int tm, int x, int j, int lane) {
     const int per = (E + 63) >> 6;
     const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
     int mine = 0;
@@ -172,8 +174,9 @@ __device__ __forceinline__ TileRows group_tile(const int32_t* offsets, int E, in
         const int o = __shfl_up(upto, d);
         if (lane >= d) upto += o;
     }
+    const int stretch = (__shfl(upto, 63) + 7) >> 3, tile = x * stretch + j;
     const uint64_t past = __ballot(upto > tile);
-    if (past == 0) return TileRows{0, 0, 0};
+    if (past == 0 || j >= stretch) return TileRows{0, 0, 0};
     const int owner = __builtin_ctzll(past);
     int left = tile - (__shfl(upto, owner) - __shfl(mine, owner));
     const int f0 = min(owner * per, E), f1 = min(f0 + per, E);
@@ -191,8 +194,8 @@ __device__ __forceinline__ TileRows group_tile(const int32_t* offsets, int E, in
 // Workgroups of a kernel that loops over the rest (a launch holds fewer than 2^32 threads).
 uint32_t grid_of(uint64_t groups) { return (uint32_t)(groups < (1u << 20) ? groups : (1u << 20)); }
 
-// A grid of one workgroup of at most 512 threads per tile.
-bool tiles_fit(uint64_t tiles) { return tiles < (1u << 23); }
+// A grid of one workgroup of at most 1024 threads per tile.
+bool tiles_fit(uint64_t tiles) { return tiles < (1u << 22); }
 
 // Compile-time loops over a constant's values.
 template <int N, class F>
@@ -221,6 +224,11 @@ __device__ __forceinline__ void* uniform_ptr(const void* p) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
     return reinterpret_cast<void*>(((uint64_t)hi << 32) | lo);
+}
+
+// Buffer resource from a row on: loads take a scalar and a 32-bit vector offset.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(p), (short)0, 0xFFFFFFFF, 0x00020000);
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -259,6 +267,7 @@ template <int ROWS, int NW>
 struct MxStager {
     static constexpr int SEGS = ROWS / 8, PER = (SEGS + NW - 1) / NW;
     uint32_t off[PER];   // byte offsets from the tile's first row at step 0
+    uint32_t end;        // offset of the operand's last block
     __amdgpu_buffer_rsrc_t rsrc;
 
     __device__ __forceinline__ static int seg(int wave, int j) { return min(wave + j * NW, SEGS - 1); }
@@ -267,69 +276,85 @@ struct MxStager {
         return block_slot(seg(wave, j) * 8 + lane / 8, lane % 8);
     }
 
-    // data: the tile's first row; last: the last row that exists, from there on
-    __device__ __forceinline__ void init(const uint8_t* data, int last, uint32_t blocks, int wave, int lane) {
-        rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(data), (short)0, 0xFFFFFFFF, 0x00020000);
+    // data: the tile's first row; last: the last row that exists, and left: the
+    // bytes of the operand, from there on
+    __device__ __forceinline__ void init(const uint8_t* data, int last, int64_t left, uint32_t blocks, int wave, int lane) {
+        rsrc = resource(data);
+        end = (uint32_t)min(left - 16, (int64_t)0xFFFFFFF0);
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             off[j] = (uint32_t)min(seg(wave, j) * 8 + lane / 8, last) * (blocks * 16) +
                      (uint32_t)block(wave, j, lane) * 16;
     }
 
-    // Before the last step, if only `left` blocks remain there: lanes whose
-    // block lies past the row's end fetch its last one.
-    __device__ __forceinline__ void clamp_to(int left, int wave, int lane) {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) off[j] -= (uint32_t)max(block(wave, j, lane) - (left - 1), 0) * 16;
-    }
-
-    // the codes of the step that starts at block c0
+    // The codes of the step that starts at block c0. If the step reaches past
+    // the rows' end (RAGGED may), what is fetched there is the next row's, or
+    // the operand's last block again; it is multiplied with zeros.
+    template <bool RAGGED>
     __device__ __forceinline__ void issue(uint32_t c0, uint8_t* lds, int wave) const {
         const uint32_t s = c0 * 16;
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off[j]), "s"(rsrc), "s"(s),
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t v = RAGGED ? min(off[j] + s, end) : off[j], c = RAGGED ? 0 : s;
+            asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(v), "s"(rsrc), "s"(c),
                          "{m0}"(lds_addr(lds) + seg(wave, j) * 1024));
-    }
-
-    // codes past the rows' end become zeros (each wave those it fetched itself)
-    __device__ __forceinline__ void zero_past(int left, uint8_t* lds, int wave, int lane) const {
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (block(wave, j, lane) >= left)
-                *reinterpret_cast<u32x4*>(lds + seg(wave, j) * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+        }
     }
 };
 
-// Scales of the BM rows of A and the BN rows of B of a tile, as [row][16] bytes
-// of a pair of steps in LDS. FULL (rows of whole steps, at least two): direct
-// loads of 16 bytes a row, one row a lane. A row of 8 bytes a step costs a
-// cache request for every 8 bytes, as many as all its codes; two steps at once
-// halve that (64 x 64 tiles, 128 x 7168 x 16384: 27 us before, 22 us after). A
-// last pair that holds only one step starts a step early, so that nothing is
-// read past a row. Otherwise in words of any alignment through registers, a
-// step at a time, scale 0 past the row's end.
-template <int BM, int BN, int NW, bool FULL>
+// How the scales of a tile's rows come to LDS, by K alone:
+enum ScalePath : int {
+    WHOLE = 0,     // K % 256 == 0, K >= 512: rows of whole steps, four-byte aligned
+    SHIFTED = 1,   // any other K >= 512: rows start at any byte
+    SHORT = 2,     // K < 512
+};
+constexpr ScalePath scale_path(uint32_t K) { return K < PAIR * 32 ? SHORT : K % (STEP * 32) == 0 ? WHOLE : SHIFTED; }
+
+// Scales of the BM rows of A and the BN rows of B of a tile, a pair of steps
+// at a time as [row][16] bytes in LDS, by direct loads, one row a lane. A row
+// of 8 bytes a step costs a cache request for every 8 bytes, as many as all
+// its codes; two steps at once halve that (64 x 64 tiles, 128 x 7168 x 16384:
+// 27 us before, 22 us after). A last pair that ends past the row starts
+// earlier, so that it ends with it.
+// SHIFTED: the loads start at the four-byte word that holds a row's first
+// scale, and one more word a row ([row][4] behind the others) holds the up to
+// three scales that the shift pushes out; a lane joins its four out of two
+// words. (The same through registers and LDS writes: 4096 x 4096 x 8224 in 92
+// us.) The last word may reach up to three bytes past the last scale of the
+// whole operand: never past the word that holds it.
+// SHORT: through registers, a step at a time, zero past the row's end.
+template <int BM, int BN, int NW, int PATH>
 struct ScaleStager {
-    static constexpr int SEGS = (BM + BN) / 64, PER = FULL ? (SEGS + NW - 1) / NW : 0;
-    static_assert(BM % 64 == 0 && BN % 64 == 0, "a stretch belongs to one operand");
+    // a stretch of 64 rows belongs to one operand: 32 rows of A take one of their own
+    static constexpr int PAD = BM < 64 ? 64 : BM;
+    static constexpr int SEGS = (PAD + BN) / 64, SPER = (SEGS + NW - 1) / NW;
+    static constexpr int PER = PATH == WHOLE ? SPER : PATH == SHIFTED ? 2 * SPER : 0;
+    static_assert(PAD % 64 == 0 && BN % 64 == 0, "whole stretches");
+    static constexpr int REST = (PAD + BN) * PAIR;                 // where the fifth words start
+    static constexpr int BYTES = REST + (PATH == SHIFTED ? (PAD + BN) * 4 : 0);
     static constexpr int WORDS = (BM + BN) * 2, WPER = (WORDS + NW * 64 - 1) / (NW * 64);
-    uint32_t off[FULL ? PER : WPER];
-    uint32_t reg[FULL ? 1 : WPER];
-    __amdgpu_buffer_rsrc_t rsrc[FULL ? PER : 1];
+    uint32_t off[PATH == SHORT ? WPER : SPER], lim[SPER];
+    uint32_t reg[PATH == SHORT ? WPER : 1];
+    __amdgpu_buffer_rsrc_t rsrc[PATH == SHORT ? 1 : SPER];
     const uint8_t *sa, *sb;
 
     __device__ __forceinline__ static int seg(int wave, int j) { return min(wave + j * NW, SEGS - 1); }
 
-    __device__ __forceinline__ void init(const uint8_t* a, const uint8_t* b, int last_a, int last_b, uint32_t blocks,
-                                         int wave, int lane) {
-        if constexpr (FULL) {
+    // a, b: the tile's first rows; last_*: the last row that exists, from
+    // there on; left_*: bytes of the operand from there on
+    __device__ __forceinline__ void init(const uint8_t* a, const uint8_t* b, int last_a, int last_b, int64_t left_a,
+                                         int64_t left_b, uint32_t blocks, int wave, int lane) {
+        if constexpr (PATH != SHORT) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
+            for (int j = 0; j < SPER; ++j) {
                 const int r = seg(wave, j) * 64;
-                const bool is_a = r < BM;
-                rsrc[j] = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(is_a ? a : b), (short)0, 0xFFFFFFFF, 0x00020000);
-                off[j] = (uint32_t)(is_a ? min(r + lane, last_a) : min(r - BM + lane, last_b)) * blocks;
+                const bool is_a = r < PAD;
+                const uint8_t* first = is_a ? a : b;
+                const uint32_t odd = PATH == SHIFTED ? (uint32_t)(reinterpret_cast<uintptr_t>(first) & 3) : 0;
+                rsrc[j] = resource(first - odd);
+                off[j] = odd + (uint32_t)(is_a ? min(r + lane, last_a) : min(r - PAD + lane, last_b)) * blocks;
+                // offset of the word that holds the operand's last scale
+                lim[j] = (uint32_t)min(odd + (is_a ? left_a : left_b) - 1, (int64_t)0x7FFFFFFF) & ~3u;
             }
         } else {
             sa = a;
@@ -344,34 +369,64 @@ struct ScaleStager {
     // first block of the pair that a step's scales are staged with
     __device__ __forceinline__ static uint32_t pair_start(int step, uint32_t blocks) {
         const uint32_t c = (uint32_t)(step / 2) * PAIR;
-        return FULL ? min(c, blocks - PAIR) : c;
+        return PATH == SHORT ? c : min(c, blocks - PAIR);
     }
     __device__ __forceinline__ void issue(uint32_t c0, uint8_t* lds, int wave) const {
+        const uint32_t c = PATH == SHIFTED ? c0 & ~3u : c0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off[j]), "s"(rsrc[j]), "s"(c0),
+        for (int j = 0; j < (PATH == SHORT ? 0 : SPER); ++j) {
+            const uint32_t v = PATH == SHIFTED ? (off[j] + (c0 & 3)) & ~3u : off[j];
+            asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(v), "s"(rsrc[j]), "s"(c),
                          "{m0}"(lds_addr(lds) + seg(wave, j) * 1024));
+            if constexpr (PATH == SHIFTED)
+                asm volatile("buffer_load_dword %0, %1, %2 offen lds" ::"v"(min(v + 16, lim[j] - c)), "s"(rsrc[j]), "s"(c),
+                             "{m0}"(lds_addr(lds) + REST + seg(wave, j) * 256));
+        }
     }
+    // SHORT: the word of a step's scales that starts at the lane's block, or
+    // the row's last whole word where that is past it; nothing waits for the load
+    __device__ __forceinline__ static uint32_t word_block(int step, int w) { return (uint32_t)(step * STEP + (w & 1) * 4); }
     __device__ __forceinline__ void fetch(int step, uint32_t blocks, int wave, int lane) {
 #pragma unroll
         for (int j = 0; j < WPER; ++j) {
             const int w = min((j * NW + wave) * 64 + lane, WORDS - 1);
             const uint8_t* q = (w / 2 < BM ? sa : sb) + off[j];
-            const uint32_t c = (uint32_t)(step * STEP + (w & 1) * 4);
             if (blocks >= 4) {
-                const uint32_t at = min(c, blocks - 4), past = c - at;      // the row's last word, shifted down
-                reg[j] = past < 4 ? *reinterpret_cast<const u32_any*>(q + at) >> (8 * past) : 0u;
+                reg[j] = *reinterpret_cast<const u32_any*>(q + min(word_block(step, w), blocks - 4));
             } else {
                 reg[j] = 0;
-                for (uint32_t b = c; b < min(c + 4, blocks); ++b) reg[j] |= (uint32_t)q[b] << (8 * (b - c));
+                for (uint32_t b = 0; b < blocks; ++b) reg[j] |= (uint32_t)q[b] << (8 * b);
             }
         }
     }
-    __device__ __forceinline__ void store(int step, uint8_t* lds, int wave, int lane) const {
+    __device__ __forceinline__ void store(int step, uint32_t blocks, uint8_t* lds, int wave, int lane) const {
 #pragma unroll
         for (int j = 0; j < WPER; ++j) {
             const int w = min((j * NW + wave) * 64 + lane, WORDS - 1);
-            *reinterpret_cast<uint32_t*>(lds + (w / 2) * 16 + (step & 1) * STEP + (w & 1) * 4) = reg[j];
+            const uint32_t c = word_block(step, w), past = c - min(c, max(blocks, 4u) - 4);
+            const int row = w / 2 + (w / 2 < BM ? 0 : PAD - BM);
+            *reinterpret_cast<uint32_t*>(lds + row * PAIR + (step & 1) * STEP + (w & 1) * 4) =
+                past < 4 ? reg[j] >> (8 * past) : 0u;
+        }
+    }
+    // Into v: the four scales from byte `at` of a pair on (the step's part of
+    // it and the lane's half) of the N rows row, row + 32, ..., whose first
+    // scale lies `odd` bytes into its word.
+    template <int N>
+    __device__ __forceinline__ static void read(const uint8_t* lds, int row, uint32_t at, uint32_t odd, int (&v)[N]) {
+        if constexpr (PATH != SHIFTED) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const int*>(lds + row * PAIR + at + 32 * PAIR * i);
+        } else {
+            const uint32_t o = at + odd, w = o >> 2;
+            const bool l4 = w < 4, h4 = w < 3;
+            const uint8_t* lo = lds + (l4 ? row * PAIR + w * 4 : REST + row * 4);
+            const uint8_t* hi = lds + (h4 ? row * PAIR + w * 4 + 4 : REST + row * 4);
+            const int ls = l4 ? 32 * PAIR : 128, hs = h4 ? 32 * PAIR : 128;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = (int)__builtin_amdgcn_alignbyte(*reinterpret_cast<const uint32_t*>(hi + hs * i),
+                                                       *reinterpret_cast<const uint32_t*>(lo + ls * i), o & 3);
         }
     }
 };
@@ -384,12 +439,11 @@ struct ScaleStager {
 // it: no vector instruction touches codes or scales between LDS and the matrix
 // cores. The steps' codes go through a ring of STAGES buffers in LDS, the
 // scales through buffers of a pair of steps, filled by direct loads.
-// FULL: K is whole steps, two at least. Otherwise the last step is finished by
-// zeroing A's blocks past the end after they landed (their scales and B's are
-// not NaN: zero, or another block's of B).
+// Where K ends inside a step, A's blocks past the end and all scales there
+// become zero in registers.
 // The matrix instruction takes B first, so a lane ends up with four
 // consecutive columns of one row of C.
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool FULL>
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int PATH>
 __global__ void __launch_bounds__(WM * WN * 64)
 mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
     constexpr int NW = WM * WN;
@@ -398,13 +452,13 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
     // A pair of scales is loaded with the codes of its first step, STAGES steps
     // ahead, and read last one step after it: so many pairs are there at once.
     constexpr int PAIRS = STAGES / 2 + 1;
-    constexpr int STAGE = (BM + BN) * 128, SCALES = (BM + BN) * PAIR;
+    constexpr int STAGE = (BM + BN) * 128, SCALES = ScaleStager<BM, BN, NW, PATH>::BYTES;
     constexpr int RING = STAGES * STAGE + PAIRS * SCALES, OUT = BM * BN * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > OUT ? RING : OUT];
     uint8_t* const scale_mem = smem + STAGES * STAGE;
     using StA = MxStager<BM, NW>;
     using StB = MxStager<BN, NW>;
-    using StS = ScaleStager<BM, BN, NW, FULL>;
+    using StS = ScaleStager<BM, BN, NW, PATH>;
     // loads a wave has in flight, at least, when only those of the STAGES - 1
     // or STAGES - 2 youngest steps are
     constexpr int L = StA::PER + StB::PER;
@@ -416,13 +470,10 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
     int tm, tn;
     TileRows t;
     if constexpr (GROUPED) {
-        // the tiles of one row of tiles share an XCD (its rows of A, and with
-        // them the expert, stay in one L2); rows of tiles are dealt out to the
-        // XCDs in turn, so the ones that do not exist are spread evenly
         const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
-        tm = (j / tiles_n) * 8 + x;
+        tm = 0;
         tn = j % tiles_n;
-        t = group_tile(p.offsets, (int)p.E, (int)p.M, BM, tm, lane);
+        t = group_tile(p.offsets, (int)p.E, (int)p.M, BM, x, j / tiles_n, lane);
         t.e = __builtin_amdgcn_readfirstlane(t.e);
         t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
         t.rows = __builtin_amdgcn_readfirstlane(t.rows);
@@ -434,7 +485,6 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
     const int n0 = tn * BN;
     const uint32_t blocks = p.K / 32;
     const int nsteps = (int)((blocks + STEP - 1) / STEP);
-    const bool ragged = !FULL && blocks % STEP != 0;
     const int64_t rb = (int64_t)t.e * p.N + n0;
     const int last_a = t.rows - 1, last_b = min(BN, (int)p.N - n0) - 1;
 
@@ -448,35 +498,27 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
         StA sa;
         StB sb;
         StS ss;
-        sa.init(p.A + (int64_t)t.row0 * blocks * 16, last_a, blocks, wave, lane);
-        sb.init(p.B + rb * blocks * 16, last_b, blocks, wave, lane);
-        ss.init(p.SFA + (int64_t)t.row0 * blocks, p.SFB + rb * blocks, last_a, last_b, blocks, wave, lane);
+        const int64_t rows_a = (int64_t)p.M - t.row0, rows_b = (int64_t)p.E * p.N - rb;     // of the operands, from here on
+        sa.init(p.A + (int64_t)t.row0 * blocks * 16, last_a, rows_a * blocks * 16, blocks, wave, lane);
+        sb.init(p.B + rb * blocks * 16, last_b, rows_b * blocks * 16, blocks, wave, lane);
+        const uint8_t *scales_a = p.SFA + (int64_t)t.row0 * blocks, *scales_b = p.SFB + rb * blocks;
+        ss.init(scales_a, scales_b, last_a, last_b, rows_a * blocks, rows_b * blocks, blocks, wave, lane);
 
         // a stage: A's codes, B's codes; before those of an even step, its pair of scales
         auto pair_mem = [&](int step) { return scale_mem + (uint32_t)(step / 2) % PAIRS * SCALES; };
         auto issue = [&](int step, uint8_t* st) {
             const int s = min(step, nsteps - 1);       // past the end: the last one again
-            if constexpr (FULL)
+            if constexpr (PATH != SHORT)
                 if ((step & 1) == 0) ss.issue(StS::pair_start(s, blocks), pair_mem(step), wave);
-            sa.issue((uint32_t)s * STEP, st, wave);
-            sb.issue((uint32_t)s * STEP, st + BM * 128, wave);
+            sa.template issue<PATH != WHOLE>((uint32_t)s * STEP, st, wave);
+            sb.template issue<PATH != WHOLE>((uint32_t)s * STEP, st + BM * 128, wave);
         };
         auto fetch = [&](int step) {
-            if constexpr (!FULL) ss.fetch(step, blocks, wave, lane);
+            if constexpr (PATH == SHORT) ss.fetch(step, blocks, wave, lane);
         };
         auto store = [&](int step) {
-            if constexpr (!FULL) ss.store(step, pair_mem(step), wave, lane);
+            if constexpr (PATH == SHORT) ss.store(step, blocks, pair_mem(step), wave, lane);
         };
-        auto clamp = [&](int step) {           // before the first issue of the last step
-            if (ragged && step == nsteps - 1) {
-                sa.clamp_to((int)(blocks % STEP), wave, lane);
-                sb.clamp_to((int)(blocks % STEP), wave, lane);
-            }
-        };
-        auto zero = [&](int step, uint8_t* st) {   // after the last step has landed
-            if (ragged && step == nsteps - 1) sa.zero_past((int)(blocks % STEP), st, wave, lane);
-        };
-
         // Fragment addresses: block 4h + s of row 32 i + l % 32 of the wave's
         // rows; every second fragment's swizzle differs in bit 2 (64 bytes).
         const int row = lane & 31, h = lane >> 5;
@@ -486,7 +528,6 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
             va[s] = (uint32_t)((wm * TM + row) * 128 + block_slot(wm * TM + row, 4 * h + s) * 16);
             vb[s] = (uint32_t)((BM + wn * TN + row) * 128 + block_slot(wn * TN + row, 4 * h + s) * 16);
         }
-        const uint32_t vsa = (uint32_t)((wm * TM + row) * PAIR + h * 4), vsb = (uint32_t)((BM + wn * TN + row) * PAIR + h * 4);
         auto frags = [&](const uint8_t* st, int s, u32x4 (&a)[FM], u32x4 (&b)[FN]) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
@@ -495,12 +536,31 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
             for (int j = 0; j < FN; ++j)
                 b[j] = *reinterpret_cast<const u32x4*>(st + (vb[s] ^ (64u * (j & 1))) + 4096 * j);
         };
+        // rows 32 apart start at the same byte of a word
+        const uint32_t odd_a = (uint32_t)reinterpret_cast<uintptr_t>(scales_a) + (uint32_t)(wm * TM + row) * blocks;
+        const uint32_t odd_b = (uint32_t)reinterpret_cast<uintptr_t>(scales_b) + (uint32_t)(wn * TN + row) * blocks;
         auto exps = [&](int step, int (&a)[FM], int (&b)[FN]) {
-            const uint8_t* q = pair_mem(step) + ((uint32_t)step * STEP - StS::pair_start(step, blocks));
+            const uint8_t* q = pair_mem(step);
+            const uint32_t ps = StS::pair_start(step, blocks), at = (uint32_t)step * STEP - ps + 4 * h;
+            StS::read(q, wm * TM + row, at, (odd_a + ps) & 3, a);
+            StS::read(q, StS::PAD + wn * TN + row, at, (odd_b + ps) & 3, b);
+            if constexpr (PATH == SHIFTED) {
+                // past the row's end: zero
+                const int left = (int)blocks - step * STEP - 4 * h;
+                const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
 #pragma unroll
-            for (int i = 0; i < FM; ++i) a[i] = *reinterpret_cast<const int*>(q + vsa + 32 * PAIR * i);
+                for (int i = 0; i < FM; ++i) a[i] &= (int)keep;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) b[j] = *reinterpret_cast<const int*>(q + vsb + 32 * PAIR * j);
+                for (int j = 0; j < FN; ++j) b[j] &= (int)keep;
+            }
+        };
+        // A's block s of the last step: zero past the row's end
+        auto cut = [&](int s, u32x4 (&a)[FM]) {
+            if constexpr (PATH != WHOLE) {
+                const uint32_t keep = 4 * h + s < (int)(blocks - (uint32_t)(nsteps - 1) * STEP) ? ~0u : 0u;
+#pragma unroll
+                for (int i = 0; i < FM; ++i) a[i] &= u32x4{keep, keep, keep, keep};
+            }
         };
         auto mfma = [&](auto sc, const u32x4 (&a)[FM], const u32x4 (&b)[FN], const int (&xa)[FM], const int (&xb)[FN]) {
             constexpr int s = decltype(sc)::value;
@@ -515,16 +575,11 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
         };
 
         fetch(0);
-        clamp(0);
         issue(0, smem);
         store(0);
 #pragma unroll
-        for (int st = 1; st < STAGES; ++st) {
-            clamp(st);
-            issue(st, smem + st * STAGE);
-        }
+        for (int st = 1; st < STAGES; ++st) issue(st, smem + st * STAGE);
         wait_vmcnt<AHEAD1>();
-        zero(0, smem);
         lds_barrier();
         fetch(1);
 
@@ -536,8 +591,6 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
             uint8_t* sn = smem + cur * STAGE;
             wait_vmcnt<AHEAD2>();                  // step k + 1 has landed for this wave ...
             store(k + 1);
-            zero(k + 1, sn);
-            clamp(k + STAGES);
             lds_barrier();                         // ... and for all, and all have read step k
             __builtin_amdgcn_sched_barrier(0);
             issue(k + STAGES, st);
@@ -556,6 +609,10 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
                 exps(k, ea[Q], eb[Q]);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) frags(st, s, fa[Q][s], fb[Q][s]);
+            };
+            auto last = [&](auto q) {
+                constexpr int Q = decltype(q)::value;
+                static_for<4>([&](auto s) { cut(decltype(s)::value, fa[Q][decltype(s)::value]); });
             };
             auto multiply = [&](auto q) {
                 constexpr int Q = decltype(q)::value;
@@ -577,8 +634,10 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
             }
             if (k + 1 < nsteps) {
                 step(k, EVEN, ODD);
+                last(ODD);
                 multiply(ODD);
             } else {
+                last(EVEN);
                 multiply(EVEN);
             }
         } else {
@@ -591,17 +650,18 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
             int ea[FM], eb[FN];
             frags(smem, 0, fa[0], fb[0]);
             exps(0, ea, eb);
-            auto leading = [&](const uint8_t* st) {
+            auto leading = [&](const uint8_t* st, auto last) {
                 static_for<3>([&](auto s) {
                     constexpr int S = decltype(s)::value;
                     frags(st, S + 1, fa[(S + 1) & 1], fb[(S + 1) & 1]);
+                    if constexpr (decltype(last)::value) cut(S, fa[S & 1]);
                     mfma(s, fa[S & 1], fb[S & 1], ea, eb);
                     interleave<FM * FN, FM + FN>();
                     __builtin_amdgcn_sched_barrier(0);
                 });
             };
             for (int k = 0; k + 1 < nsteps; ++k) {
-                leading(smem + cur * STAGE);
+                leading(smem + cur * STAGE, std::false_type{});
                 const uint8_t* sn = advance(k);
                 int xa[FM], xb[FN];
                 frags(sn, 0, fa[0], fb[0]);
@@ -614,7 +674,8 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
 #pragma unroll
                 for (int j = 0; j < FN; ++j) eb[j] = xb[j];
             }
-            leading(smem + cur * STAGE);
+            leading(smem + cur * STAGE, std::true_type{});
+            cut(3, fa[1]);
             mfma(std::integral_constant<int, 3>{}, fa[1], fb[1], ea, eb);
         }
         wait_vmcnt<0>();       // what was loaded past the end lands before LDS is used again
@@ -659,73 +720,56 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
     }
 }
 
-// Few rows: the weights' bytes are the time, so they go straight from memory
-// into the registers of the one wave that multiplies them, and enough of them
-// are in flight at once. A workgroup owns 16 columns and up to 16 MT rows; its
-// NW waves take K in turns of 512 elements (16 blocks), and the sums meet in
-// LDS, added in the waves' order. The matrix instruction is 16 x 16 x 128: lane
-// l of instruction s of a turn holds block 4s + l / 16 of row l % 16, so a load
-// of the wave covers 64 consecutive bytes of 16 rows, and its scale is byte
-// l / 16 of word s of the row's 16 scale bytes of the turn.
-template <int MT, int NW, bool GROUPED>
+// Few rows and few columns: the weights' bytes are the time, so they go
+// straight from memory into the registers of the one wave that multiplies
+// them, and K is shared out so that enough of them are in flight at once. A
+// workgroup owns 16 columns and up to 16 rows; its NW waves take K in turns of
+// 512 elements (16 blocks), and the sums meet in LDS, added in the waves'
+// order. The matrix instruction is 16 x 16 x 128: lane l of instruction s of a
+// turn holds block 4s + l / 16 of row l % 16, so a load of the wave covers 64
+// consecutive bytes of 16 rows, and its scale is byte l / 16 of word s of the
+// row's 16 scale bytes of the turn.
+template <int NW>
 __global__ void __launch_bounds__(NW * 64)
 mx_skinny_kernel(MxGemmProblem p, int tiles_n) {
     constexpr int TURN = 16;                       // blocks per turn
-    __shared__ f32x4 part[NW][MT][64];
+    __shared__ f32x4 part[NW][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
-    TileRows t{0, tm * 16 * MT, min(16 * MT, (int)p.M - tm * 16 * MT)};
-    if constexpr (GROUPED) {
-        t = group_tile(p.offsets, (int)p.E, (int)p.M, 16 * MT, tm, lane);
-        if (t.rows <= 0) return;
-    }
-    const int n0 = tn * 16, r = lane & 15, g = lane >> 4;
+    const int m0 = (int)blockIdx.x / tiles_n * 16, n0 = (int)blockIdx.x % tiles_n * 16;
+    const int r = lane & 15, g = lane >> 4;
     const uint32_t blocks = p.K / 32;
-    const int64_t rb = (int64_t)t.e * p.N + min(n0 + r, (int)p.N - 1);
+    const int64_t ra = min(m0 + r, (int)p.M - 1), rb = min(n0 + r, (int)p.N - 1);
+    const uint8_t *a = p.A + ra * blocks * 16, *sa = p.SFA + ra * blocks;
     const uint8_t *b = p.B + rb * blocks * 16, *sb = p.SFB + rb * blocks;
-    const uint8_t *a[MT], *sa[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t ra = t.row0 + min(16 * i + r, t.rows - 1);
-        a[i] = p.A + ra * blocks * 16;
-        sa[i] = p.SFA + ra * blocks;
-    }
-    f32x4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
-    auto mfma = [&](const u32x4& x, const u32x4& y, int ex, int ey, f32x4& c) {
+    f32x4 acc = {};
+    auto mfma = [&](const u32x4& x, const u32x4& y, int ex, int ey) {
         const i32x8 X = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
         const i32x8 Y = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
-        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(Y, X, c, 4, 4, 0, ey, 0, ex);
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(Y, X, acc, 4, 4, 0, ey, 0, ex);
     };
     // whole turns, the next one's loads in flight during a turn's products
-    u32x4 wb[2][4], wa[2][MT][4], eb[2], ea[2][MT];
-    auto load = [&](uint32_t c0, int q) {
+    u32x4 wa[2][4], wb[2][4], ea[2], eb[2];
+    auto load = [&](uint32_t turn, int q) {
+        const uint32_t c0 = turn * TURN;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) wb[q][s] = *reinterpret_cast<const u32x4*>(b + (uint64_t)(c0 + 4 * s + g) * 16);
-        eb[q] = *reinterpret_cast<const u32x4_any*>(sb + c0);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                wa[q][i][s] = *reinterpret_cast<const u32x4*>(a[i] + (uint64_t)(c0 + 4 * s + g) * 16);
-            ea[q][i] = *reinterpret_cast<const u32x4_any*>(sa[i] + c0);
+        for (int s = 0; s < 4; ++s) {
+            wb[q][s] = *reinterpret_cast<const u32x4*>(b + (uint64_t)(c0 + 4 * s + g) * 16);
+            wa[q][s] = *reinterpret_cast<const u32x4*>(a + (uint64_t)(c0 + 4 * s + g) * 16);
         }
+        eb[q] = *reinterpret_cast<const u32x4_any*>(sb + c0);
+        ea[q] = *reinterpret_cast<const u32x4_any*>(sa + c0);
     };
     auto multiply = [&](int q) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                mfma(wa[q][i][s], wb[q][s], (int)(ea[q][i][s] >> (8 * g)), (int)(eb[q][s] >> (8 * g)), acc[i]);
+        for (int s = 0; s < 4; ++s) mfma(wa[q][s], wb[q][s], (int)(ea[q][s] >> (8 * g)), (int)(eb[q][s] >> (8 * g)));
     };
     const uint32_t turns = blocks / TURN;
     uint32_t u = wave;
-    if (u < turns) load(u * TURN, 0);
+    if (u < turns) load(u, 0);
     for (; u + NW < turns; u += 2 * NW) {
-        load((u + NW) * TURN, 1);
+        load(u + NW, 1);
         multiply(0);
-        if (u + 2 * NW < turns) load((u + 2 * NW) * TURN, 0);
+        if (u + 2 * NW < turns) load(u + 2 * NW, 0);
         multiply(1);
     }
     if (u < turns) multiply(0);
@@ -735,58 +779,54 @@ mx_skinny_kernel(MxGemmProblem p, int tiles_n) {
         for (int s = 0; s < 4; ++s) {
             const uint32_t c = turns * TURN + 4 * s + g, cc = min(c, blocks - 1);
             const u32x4 y = *reinterpret_cast<const u32x4*>(b + (uint64_t)cc * 16);
-            const int ey = sb[cc];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                u32x4 x = *reinterpret_cast<const u32x4*>(a[i] + (uint64_t)cc * 16);
-                if (c >= blocks) x = u32x4{0u, 0u, 0u, 0u};
-                mfma(x, y, sa[i][cc], ey, acc[i]);
-            }
+            u32x4 x = *reinterpret_cast<const u32x4*>(a + (uint64_t)cc * 16);
+            if (c >= blocks) x = u32x4{0u, 0u, 0u, 0u};
+            mfma(x, y, sa[cc], sb[cc]);
         }
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    part[wave][lane] = acc;
     __syncthreads();
-    // lane l of a 16 x 16 result holds columns 4 (l / 16) .. + 3 of row l % 16
-    for (int q = threadIdx.x; q < MT * 64; q += NW * 64) {
-        const int i = q >> 6, l = q & 63;
-        f32x4 c = part[0][i][l];
+    if (wave != 0) return;
+    // lane l of the result holds columns 4 (l / 16) .. + 3 of row l % 16
 #pragma unroll
-        for (int w = 1; w < NW; ++w) c += part[w][i][l];
-        const int m = 16 * i + (l & 15), n = n0 + 4 * (l >> 4);
-        if (m >= t.rows) continue;
-        uint16_t* out = p.C + (int64_t)(t.row0 + m) * p.N + n;
-        const u32x2 w = {pack_bf16x2(c.x, c.y), pack_bf16x2(c.z, c.w)};
-        if (n + 4 <= (int)p.N)
-            *reinterpret_cast<u32x2_any*>(out) = w;
-        else
-            for (int e = 0; n + e < (int)p.N; ++e) out[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
-    }
+    for (int w = 1; w < NW; ++w) acc += part[w][lane];
+    const int m = m0 + r, n = n0 + 4 * g;
+    if (m >= (int)p.M) return;
+    uint16_t* out = p.C + (int64_t)m * p.N + n;
+    const u32x2 w = {pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w)};
+    if (n + 4 <= (int)p.N)
+        *reinterpret_cast<u32x2_any*>(out) = w;
+    else
+        for (int e = 0; n + e < (int)p.N; ++e) out[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
 }
 
-template <int MT, int NW>
+template <int NW>
 hipError_t launch_skinny(const MxGemmProblem& p, hipStream_t stream) {
-    const uint64_t tiles_n = (p.N + 15) / 16;
-    const uint64_t tiles_m = p.offsets != nullptr ? p.M / (16 * MT) + (p.E < p.M ? p.E : p.M) : (p.M + 16 * MT - 1) / (16 * MT);
-    if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
-    auto k = p.offsets != nullptr ? mx_skinny_kernel<MT, NW, true> : mx_skinny_kernel<MT, NW, false>;
-    k<<<dim3((uint32_t)(tiles_m * tiles_n)), NW * 64, 0, stream>>>(p, (int)tiles_n);
+    const uint64_t tiles_n = (p.N + 15) / 16, tiles_m = (p.M + 15) / 16;
+    mx_skinny_kernel<NW><<<dim3((uint32_t)(tiles_m * tiles_n)), NW * 64, 0, stream>>>(p, (int)tiles_n);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+// WM x WN waves where K is whole steps, WM2 x WN2 otherwise (more registers:
+// fewer, larger waves keep two workgroups on a compute unit, or avoid spills).
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int WM2 = WM, int WN2 = WN>
 hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
     const uint64_t tiles_n = (p.N + BN - 1) / BN;
-    // every expert may end in a partly filled tile
-    uint64_t tiles_m = p.offsets != nullptr ? p.M / BM + (p.E < p.M ? p.E : p.M) : (p.M + BM - 1) / BM;
-    if (p.offsets != nullptr) tiles_m = (tiles_m + 7) / 8 * 8;      // whole turns over the XCDs
+    uint64_t tiles_m = (p.M + BM - 1) / BM;
+    if (GROUPED) {
+        // every expert may end in a partly filled tile; eight stretches of at
+        // least as many tiles as exist
+        tiles_m = (p.M / BM + (p.E < p.M ? p.E : p.M) + 7) / 8 * 8;
+    }
     if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
-    const bool full = p.K % (STEP * 32) == 0 && p.K >= PAIR * 32;
-    auto k = p.offsets != nullptr ? (full ? mx_tile_kernel<BM, BN, WM, WN, STAGES, true, true>
-                                           : mx_tile_kernel<BM, BN, WM, WN, STAGES, true, false>)
-                                  : (full ? mx_tile_kernel<BM, BN, WM, WN, STAGES, false, true>
-                                           : mx_tile_kernel<BM, BN, WM, WN, STAGES, false, false>);
-    k<<<dim3((uint32_t)(tiles_m * tiles_n)), WM * WN * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+    const dim3 grid((uint32_t)(tiles_m * tiles_n));
+    const ScalePath path = scale_path(p.K);
+    if (path == WHOLE)
+        mx_tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, WHOLE><<<grid, WM * WN * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+    else if (path == SHIFTED)
+        mx_tile_kernel<BM, BN, WM2, WN2, STAGES, GROUPED, SHIFTED><<<grid, WM2 * WN2 * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+    else
+        mx_tile_kernel<BM, BN, WM2, WN2, STAGES, GROUPED, SHORT><<<grid, WM2 * WN2 * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
     return hipGetLastError();
 }
 
@@ -816,32 +856,34 @@ hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
 }
 
 hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
-    const uint32_t turns = (p.K + 511) / 512;
     if (p.offsets != nullptr) {
-        // by the rows an expert has on average
+        // By the rows an expert has on average. 256 experts, N 1024, K 2048,
+        // us with 32 x 128, 64 x 128 and 128 x 128 tiles: 4 rows 51, 52, 55;
+        // 16 rows 59, 59, 65; 32 rows 72, 67, 73; 141 rows 161, 126, 118.
         const uint64_t mean = p.M / p.E;
-        if (mean <= 8) return turns >= 8 ? launch_skinny<1, 8>(p, stream) : launch_skinny<1, 4>(p, stream);
-        if (mean <= 48) return launch_tile<64, 64, 2, 2, 4>(p, stream);
-        return launch_tile<128, 128, 4, 2, 2>(p, stream);
+        if (mean < 16) return launch_tile<32, 128, 1, 4, 2, true>(p, stream);
+        if (mean < 64) return launch_tile<64, 128, 2, 2, 3, true>(p, stream);
+        return launch_tile<128, 128, 4, 2, 2, true, 2, 2>(p, stream);
     }
-    // Up to 16 rows, and up to 32 where the 64-column tiles would be few:
-    // 1 x 4096 x 7168 5.0 us against 9.7 us with the smallest tile, 16 x 4096 x
-    // 7168 6.3 / 9.7 us, 32 x 4096 x 7168 8.4 / 9.8 us (32 x 12288 x 2048: 9.5 / 5.4 us).
-    if (p.M <= 16) return turns >= 8 ? launch_skinny<1, 8>(p, stream) : launch_skinny<1, 4>(p, stream);
-    if (p.M <= 32 && (uint64_t)p.N * 3 < (uint64_t)p.cus * 64) return launch_skinny<2, 4>(p, stream);
-    // The tile whose time, counted in rounds over the compute units, is least:
-    // us per tile and per step of 256 K elements, alone on a compute unit and
-    // as one of two (fitted to 20 shapes, 64 x 4096 x 7168 to 4096 x 4096 x 8192).
+    // Up to 16 rows, where 64-column tiles would fill under a third of the
+    // compute units: 1 x 4096 x 7168 5.0 us against 8.0 us with the smallest
+    // tile, 16 x 4096 x 7168 6.3 / 8.1 us (16 x 7168 x 16384: 20 / 15 us).
+    if (p.M <= 16 && (uint64_t)p.N * 3 <= (uint64_t)p.cus * 64)
+        return p.K >= 8 * 512 ? launch_skinny<8>(p, stream) : launch_skinny<4>(p, stream);
+    // Otherwise the tile whose time, counted in rounds over the compute units,
+    // is least: us per tile and per step of 256 K elements, alone on a compute
+    // unit and as one of two (fitted to 20 shapes from 32 x 4096 x 7168 to
+    // 4096 x 4096 x 8192, most within 10%).
     struct Tile {
         int bm, bn;
         double fixed, alone, paired;   // paired 0: one workgroup fills a compute unit's LDS
     };
-    static constexpr Tile tiles[] = {{256, 256, 4.0, 2.15, 0}, {256, 128, 2.1, 1.19, 0}, {128, 128, 2.0, 0.68, 1.3},
-                                     {128, 64, 2.5, 0.45, 0.77}, {64, 64, 1.5, 0.31, 0.54}};
+    static constexpr Tile tiles[] = {{256, 256, 4.0, 2.15, 0},    {256, 128, 2.1, 1.19, 0},   {128, 128, 2.0, 0.68, 1.3},
+                                     {128, 64, 2.5, 0.45, 0.77}, {64, 64, 1.5, 0.31, 0.54}, {32, 64, 1.5, 0.23, 0.4}};
     const double steps = (p.K + 255) / 256;
     int best = 0;
     double least = 0;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 6; ++i) {
         const Tile& c = tiles[i];
         const uint64_t n = (uint64_t)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn), cu = p.cus;
         double t;
@@ -855,12 +897,13 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
         if (i == 0 || t < least) best = i, least = t;
     }
     switch (best) {
-        case 0: return launch_tile<256, 256, 2, 4, 2>(p, stream);
-        case 1: return launch_tile<256, 128, 4, 2, 2>(p, stream);
-        case 2: return launch_tile<128, 128, 4, 2, 2>(p, stream);
-        case 3: return launch_tile<128, 64, 2, 2, 3>(p, stream);
+        case 0: return launch_tile<256, 256, 2, 4, 2, false, 2, 2>(p, stream);
+        case 1: return launch_tile<256, 128, 4, 2, 2, false>(p, stream);
+        case 2: return launch_tile<128, 128, 4, 2, 2, false, 2, 2>(p, stream);
+        case 3: return launch_tile<128, 64, 2, 2, 3, false>(p, stream);
+        case 4: return launch_tile<64, 64, 2, 2, 4, false>(p, stream);
     }
-    return launch_tile<64, 64, 2, 2, 4>(p, stream);
+    return launch_tile<32, 64, 1, 2, 4, false>(p, stream);
 }
 
 }  // namespace bg
