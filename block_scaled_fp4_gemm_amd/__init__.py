@@ -137,14 +137,15 @@ def _f32(t: torch.Tensor, what: str) -> torch.Tensor:
 
 
 def _shape(t: torch.Tensor, shape, what: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _dims(t: torch.Tensor, n: int, what: str):
-    if t.dim() != n:
-        raise ValueError(f"{what} must be {n}-D, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{what} must be {n}-D, got shape {tuple(shape)}")
+    return shape
 
 
 # torch's raw accessors for the current device and stream (the public
@@ -161,6 +162,18 @@ def _current_device() -> int:
 def _on_device(*ts) -> None:
     """Every tensor (None skipped) is on the current HIP device (contiguity is
     checked where its pointer is taken, in _ptr)."""
+    cur = None
+    for t in ts:
+        if t is not None:
+            d = t.get_device()
+            if d != cur or d < 0:
+                if cur is None and d >= 0:
+                    cur = _current_device()
+                if d != cur:
+                    _wrong_device(ts)
+
+
+def _wrong_device(ts) -> None:
     ts = [t for t in ts if t is not None]
     for t in ts:
         if not t.is_cuda:
@@ -490,17 +503,23 @@ def bf16_scaled_add(out: torch.Tensor, delta: torch.Tensor, scale: float, stream
     return out
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A new tensor for a call on `stream` (None: the current one). Memory of
-    torch's pool belongs to the stream it was taken on: taken on another one,
-    it could still be in use there, or be handed out there again while the
-    call runs."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+class _on_stream:
+    """Context in which new tensors are taken for a call on `stream` (None: the
+    current one). Memory of torch's pool belongs to the stream it was taken on:
+    taken on another one, it could still be in use there, or be handed out
+    there again while the call runs."""
+
+    def __new__(cls, stream, device):
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        return torch.cuda.stream(stream)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    with _on_stream(stream, like.device):
+        return like.new_empty(shape, dtype=dtype)
 
 
 # ---------------------------------------------------------------------------
@@ -511,15 +530,14 @@ _BG_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # bg_type
 
 
 def _type(t: torch.Tensor, what: str) -> int:
-    _tensor(t, what)
-    if t.dtype not in _BG_TYPES:
+    kind = _BG_TYPES.get(_tensor(t, what).dtype)
+    if kind is None:
         raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
-    return _BG_TYPES[t.dtype]
+    return kind
 
 
 def _i32(t: torch.Tensor, what: str) -> torch.Tensor:
-    _tensor(t, what)
-    if t.dtype != torch.int32:
+    if _tensor(t, what).dtype != torch.int32:
         raise TypeError(f"{what}: expected int32, got {t.dtype}")
     return t
 
@@ -529,13 +547,12 @@ def _blocks32(k: int) -> None:
         raise ValueError(f"K = {k} must be a multiple of 32 (one scale per 32 elements)")
 
 
-def _mx_operands(a, sfa, b, sfb, experts: bool):
+def _mx_operands(a, sfa, b, sfb, nd: int):
     """Shapes of MXFP4 operands: A [M, K/2], SFA [M, K/32], B [(E,) N, K/2], SFB [(E,) N, K/32]."""
     m, kh = _dims(_bytes(a, "A"), 2, "A")
-    _dims(_bytes(b, "B"), 3 if experts else 2, "B")
+    *lead, _ = _dims(_bytes(b, "B"), nd, "B")
     k = 2 * kh
     _blocks32(k)
-    lead = tuple(b.shape[:-1])
     _shape(b, (*lead, kh), "B")
     _shape(_bytes(sfa, "SFA"), (m, k // 32), "SFA")
     _shape(_bytes(sfb, "SFB"), (*lead, k // 32), "SFB")
@@ -548,18 +565,19 @@ def mxfp4_quantize(x: torch.Tensor, rows: torch.Tensor | None = None, out: torch
     stride). With `rows` (int32 [R]), row i of the result is x[rows[i]], all zero where rows[i] is not a
     row of x; without, R = M."""
     kind = _type(x, "x")
-    _dims(x, 2, "x")
-    m, k, ldx = _rows(x, "x")
+    r, k = _dims(x, 2, "x")
+    m, k, ldx = (r, k, k) if x.is_contiguous() else _rows(x, "x")
     _blocks32(k)
-    r = m
     if rows is not None:
         (r,) = _dims(_i32(rows, "rows"), 1, "rows")
     if out is None:
-        out = _empty((r, k // 2), torch.uint8, x.device, stream)
+        out = _new(x, (r, k // 2), torch.uint8, stream)
+    else:
+        _shape(_bytes(out, "out"), (r, k // 2), "out")
     if scales is None:
-        scales = _empty((r, k // 32), torch.uint8, x.device, stream)
-    _shape(_bytes(out, "out"), (r, k // 2), "out")
-    _shape(_bytes(scales, "scales"), (r, k // 32), "scales")
+        scales = _new(x, (r, k // 32), torch.uint8, stream)
+    else:
+        _shape(_bytes(scales, "scales"), (r, k // 32), "scales")
     _on_device(x, rows, out, scales)
     if r == 0:      # an empty row list has no address, which the library would take for no list
         return out, scales
@@ -576,9 +594,10 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
     _blocks32(k)
     _shape(_bytes(scales, "scales"), (m, k // 32), "scales")
     if out is None:
-        out = _empty((m, k), dtype, codes.device, stream)
+        out = _new(codes, (m, k), dtype, stream)
+    else:
+        _shape(out, (m, k), "out")
     kind = _type(out, "out")
-    _shape(out, (m, k), "out")
     _on_device(codes, scales, out)
     _check(lib.mxfp4_dequantize(_ptr(codes), _ptr(scales), _ptr(out), kind, m, k, _stream(stream)),
            "mxfp4_dequantize")
@@ -588,10 +607,11 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
 def gemm_mxfp4(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
                out: torch.Tensor | None = None, stream=None):
     """C = bf16(deq(A) @ deq(B)^T): A [M, K/2] packed e2m1, SFA [M, K/32] e8m0, B [N, K/2], SFB [N, K/32]."""
-    (n,), m, k = _mx_operands(a, sfa, b, sfb, experts=False)
+    (n,), m, k = _mx_operands(a, sfa, b, sfb, 2)
     if out is None:
-        out = _empty((m, n), torch.bfloat16, a.device, stream)
-    _shape(_bits16(out, "out"), (m, n), "out")
+        out = _new(a, (m, n), torch.bfloat16, stream)
+    else:
+        _shape(_bits16(out, "out"), (m, n), "out")
     _on_device(a, sfa, b, sfb, out)
     _check(lib.gemm_mxfp4(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(out), m, n, k, _stream(stream)),
            "gemm_mxfp4")
@@ -603,11 +623,12 @@ def gemm_mxfp4_grouped(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb:
     """Rows offsets[e] .. offsets[e+1]-1 of A [S, K/2] times expert e of B [E, N, K/2] (scales SFA [S, K/32],
     SFB [E, N, K/32], offsets int32 [E + 1] on the device) -> bf16 [S, N]. Rows before offsets[0] and from
     offsets[E] on are not written."""
-    (e, n), s, k = _mx_operands(a, sfa, b, sfb, experts=True)
+    (e, n), s, k = _mx_operands(a, sfa, b, sfb, 3)
     _shape(_i32(offsets, "offsets"), (e + 1,), "offsets")
     if out is None:
-        out = _empty((s, n), torch.bfloat16, a.device, stream)
-    _shape(_bits16(out, "out"), (s, n), "out")
+        out = _new(a, (s, n), torch.bfloat16, stream)
+    else:
+        _shape(_bits16(out, "out"), (s, n), "out")
     _on_device(a, sfa, b, sfb, offsets, out)
     _check(lib.gemm_mxfp4_grouped(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(offsets), _ptr(out), s, n, k, e,
                                   _stream(stream)), "gemm_mxfp4_grouped")
@@ -642,6 +663,21 @@ def moe_route_workspace_bytes(t: int, e: int) -> int:
     return int(lib.moe_route_workspace_bytes(t, e))
 
 
+def _new_routing(logits: torch.Tensor, t: int, e: int, k: int):
+    """The tensors of a MoeRouting, and their addresses. Arrays of a kind share one allocation (a
+    caching allocation costs the host more than a view)."""
+    i32, f32 = torch.int32, torch.float32
+    choices, whole = logits.new_empty((3, t, k), dtype=i32), logits.new_empty(2 * e + 2, dtype=i32)
+    weights, real = logits.new_empty((t, k), dtype=f32), logits.new_empty(e + 1, dtype=f32)
+    ids, pos, rows = choices.unbind(0)
+    counts, offsets, n_valid = whole.split_with_sizes((e, e + 1, 1))
+    mean_probs, loss = real.split_with_sizes((e, 1))
+    c, w, r = choices.data_ptr(), whole.data_ptr(), real.data_ptr()
+    n = 4 * t * k
+    return ((ids, weights, counts, offsets, rows.view(-1), pos, mean_probs, loss.view(()), n_valid.view(())),
+            _RoutingPointers(c, weights.data_ptr(), w, w + 4 * e, c + 2 * n, c + n, r, r + 4 * e, w + 8 * e + 4))
+
+
 def moe_route(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None, normalize: bool = True,
               workspace: torch.Tensor | None = None, stream=None) -> MoeRouting:
     """Top-k routing of router logits [T, E] (bfloat16 or float32): choices, weights, per-expert counts, the
@@ -657,20 +693,18 @@ def moe_route(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None, n
             raise TypeError(f"valid: expected bool or bytes, got {valid.dtype}")
         _shape(valid, (t,), "valid")
     _on_device(logits, valid, workspace)
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
     if workspace is None:
         need = moe_route_workspace_bytes(t, e)
-        workspace = _empty(need, torch.uint8, dev, stream) if need else None
-    r = MoeRouting(_empty((t, k), i32, dev, stream), _empty((t, k), f32, dev, stream),
-                   _empty(e, i32, dev, stream), _empty(e + 1, i32, dev, stream),
-                   _empty(t * k, i32, dev, stream), _empty((t, k), i32, dev, stream),
-                   _empty(e, f32, dev, stream), _empty((), f32, dev, stream),
-                   _empty((), i32, dev, stream), k, bool(normalize))
-    ptrs = _RoutingPointers(*[x.data_ptr() for x in r[:9]])
+        workspace = _new(logits, need, torch.uint8, stream) if need else None
+    if stream is None:
+        tensors, ptrs = _new_routing(logits, t, e, k)
+    else:
+        with _on_stream(stream, logits.device):
+            tensors, ptrs = _new_routing(logits, t, e, k)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.moe_route(_ptr(logits), kind, _ptr(valid), ctypes.byref(ptrs), _ptr(workspace), ws_bytes, t, e, k,
-                         int(r.normalize), _stream(stream)), "moe_route")
-    return r
+                         1 if normalize else 0, _stream(stream)), "moe_route")
+    return MoeRouting(*tensors, k, bool(normalize))
 
 
 def moe_route_backward(logits: torch.Tensor, routing: MoeRouting, dweights: torch.Tensor | None = None,
@@ -689,14 +723,15 @@ def moe_route_backward(logits: torch.Tensor, routing: MoeRouting, dweights: torc
     if dloss is not None and _f32(dloss, "dloss").numel() != 1:
         raise ValueError(f"dloss must hold one value, got shape {tuple(dloss.shape)}")
     if out is None:
-        out = _empty((t, e), logits.dtype, logits.device, stream)
-    if _type(out, "out") != kind:
+        out = _new(logits, (t, e), logits.dtype, stream)
+    elif _type(out, "out") != kind:
         raise TypeError(f"out: expected {logits.dtype}, got {out.dtype}")
-    _shape(out, (t, e), "out")
+    else:
+        _shape(out, (t, e), "out")
     _on_device(logits, routing.ids, routing.weights, routing.counts, routing.n_valid, dweights, dloss, out)
     _check(lib.moe_route_backward(_ptr(logits), kind, _ptr(routing.ids), _ptr(routing.weights), _ptr(routing.counts),
                                   _ptr(routing.n_valid), _ptr(dweights), _ptr(dloss), _ptr(out), t, e, routing.k,
-                                  int(routing.normalize), _stream(stream)), "moe_route_backward")
+                                  1 if routing.normalize else 0, _stream(stream)), "moe_route_backward")
     return out
 
 
