@@ -104,16 +104,17 @@ constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 
 constexpr uint32_t kMaxExperts = 1024;   // routing and grouped products
 constexpr uint32_t kMaxTopK = 16;
 
-// Rows per workgroup of moe_route: 16 at least (one pass of a workgroup), and
-// for long batches more, at most 128, so that the per-workgroup counts and
-// sums that the workspace holds stay small against the logits.
-inline uint32_t route_rows_per_block(uint32_t T) {
-    const uint32_t want = (T + 1023) / 1024;              // about 1024 workgroups
-    const uint32_t r = (want + 15) / 16 * 16;
-    return r < 16 ? 16 : r > 128 ? 128 : r;
-}
 // Up to this many rows one workgroup routes alone, in one launch, without a workspace.
-constexpr uint32_t kRouteOneBlock = 32;
+constexpr uint32_t kRouteOneBlock = 64;
+// Above this many rows the workgroups of moe_route have 1024 threads, else 256.
+constexpr uint32_t kRouteWide = 8192;
+// Rows per workgroup of moe_route: at most 256 workgroups, so that each can
+// sum the counts of all the others by itself, of whole passes (16 tokens per
+// 256 threads where 16 lanes hold one).
+inline uint32_t route_rows_per_block(uint32_t T) {
+    const uint32_t pass = T > kRouteWide ? 64 : 16;
+    return ((T + 255) / 256 + pass - 1) / pass * pass;
+}
 inline uint32_t route_blocks(uint32_t T) {
     if (T <= kRouteOneBlock) return 1;
     const uint32_t r = route_rows_per_block(T);
