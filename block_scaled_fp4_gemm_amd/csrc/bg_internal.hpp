@@ -106,23 +106,29 @@ constexpr uint32_t kMaxTopK = 16;
 
 // Up to this many rows one workgroup routes alone, in one launch, without a workspace.
 constexpr uint32_t kRouteOneBlock = 64;
-// Above this many rows the workgroups of moe_route have 1024 threads, else 256.
-constexpr uint32_t kRouteWide = 8192;
-// Rows per workgroup of moe_route: at most 256 workgroups, so that each can
-// sum the counts of all the others by itself, of whole passes (16 tokens per
-// 256 threads where 16 lanes hold one).
+// Above this many rows the workgroups of moe_route have 1024 threads, else 512.
+constexpr uint32_t kRouteWide = 16384;
+// Rows per workgroup of moe_route: 256 workgroups at most, so that each can sum
+// the counts of all the others by itself, of whole passes (32 tokens per 512
+// threads where 16 lanes hold one), but fewer than 2^16 rows, so that counts
+// fit 16 bits.
+constexpr uint32_t kRouteMaxRows = 65472;
 inline uint32_t route_rows_per_block(uint32_t T) {
-    const uint32_t pass = T > kRouteWide ? 64 : 16;
-    return ((T + 255) / 256 + pass - 1) / pass * pass;
+    const uint32_t pass = T > kRouteWide ? 64 : 32;
+    const uint32_t rows = (T / 256 + (T % 256 != 0) + pass - 1) / pass * pass;
+    return rows < kRouteMaxRows ? rows : kRouteMaxRows;
 }
 inline uint32_t route_blocks(uint32_t T) {
     if (T <= kRouteOneBlock) return 1;
     const uint32_t r = route_rows_per_block(T);
-    return (T + r - 1) / r;
+    return T / r + (T % r != 0);
 }
-// Per workgroup: E counts, E sums of probabilities, and the number of live rows.
+// Per workgroup: E sums of probabilities, the number of live rows (the whole
+// rounded up to 16 bytes), E counts of 16 bits.
 inline size_t route_workspace_bytes(uint32_t T, uint32_t E) {
-    return T <= kRouteOneBlock ? 0 : (size_t)route_blocks(T) * (2 * (size_t)E + 1) * 4;
+    if (T <= kRouteOneBlock) return 0;
+    const size_t n = route_blocks(T);
+    return n * E * 4 + (n + 3) / 4 * 16 + n * E * 2;
 }
 
 // Size of the library-owned split-K scratch of gemm_bf16_splitk_noalloc, per

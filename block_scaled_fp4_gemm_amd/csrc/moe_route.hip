@@ -23,6 +23,13 @@
 // the second sums the counts of the workgroups before its own, ranks the
 // choices among its rows and writes the places; one more workgroup of it adds
 // the statistics. All sums over rows are added in a fixed order.
+//
+// Measured, 256 experts, k = 8, BF16 logits, 65536 / 4510 rows: the first
+// kernel 22.9 / 6.8 us (bound by the choices' vector operations: 1.5 TB/s), the
+// second 15.3 / 10.1 (latencies: the sums, then places scattered over 2 MB),
+// the gradient 19.1 / 7.7 (3.5 TB/s of logits, gradients and choices). With
+// FP32 logits the first takes 33.4 and the gradient 33.7 (4 TB/s). One launch
+// does 16 rows in 8.6.
 #include <type_traits>
 
 #include "bg_internal.hpp"
@@ -119,15 +126,18 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
             }
         }
     } else {
+        // every lane loads (past E, the row's last logit again): a branch
+        // around each load would wait for one after the other
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            if (e0 + i >= E)
-                v[i] = NEG_INF;
-            else if constexpr (F32)
-                v[i] = static_cast<const float*>(logits)[t * E + e0 + i];
+            const int64_t at = t * E + min(e0 + i, E - 1);
+            if constexpr (F32)
+                v[i] = static_cast<const float*>(logits)[at];
             else
-                v[i] = __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(logits)[t * E + e0 + i] << 16);
+                v[i] = __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
         }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? v[i] : NEG_INF;
     }
 }
 
@@ -195,21 +205,24 @@ struct TopK<true, G, VPL> {
     }
 };
 
-// Workspace of the two-kernel form: [blocks][E] counts, [blocks][E] sums of
-// probabilities, [blocks] live rows.
+// Workspace of the two-kernel form: [blocks][E] sums of probabilities, [blocks]
+// live rows, [blocks][E] counts (16 bits: a workgroup has fewer than 2^16 rows).
 struct RouteWs {
-    int32_t* hist;
+    uint16_t* hist;
     float* psum;
     int32_t* live;
 };
 
 __device__ inline RouteWs split_ws(void* ws, uint64_t blocks, uint32_t E) {
     RouteWs w;
-    w.hist = static_cast<int32_t*>(ws);
-    w.psum = reinterpret_cast<float*>(w.hist + blocks * E);
+    w.psum = static_cast<float*>(ws);
     w.live = reinterpret_cast<int32_t*>(w.psum + blocks * E);
+    w.hist = reinterpret_cast<uint16_t*>(w.live + (blocks + 3) / 4 * 4);
     return w;
 }
+
+// A barrier that orders LDS only: nothing waits for stores to memory.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Exclusive prefix over the E counts in LDS, in place: counts -> offsets
 // (E + 1 values). At least 256 threads call it; E <= 1024, four per thread.
@@ -229,7 +242,7 @@ __device__ __forceinline__ void scan_counts(int32_t* c, int E, int tid) {
         if (lane >= d) upto += o;
     }
     if (lane == 63 && tid < 256) part[tid >> 6] = upto;
-    __syncthreads();
+    lds_barrier();
     if (tid < 256) {
         int base = upto - mine;
         for (int w = 0; w < (tid >> 6); ++w) base += part[w];
@@ -240,52 +253,56 @@ __device__ __forceinline__ void scan_counts(int32_t* c, int E, int tid) {
         }
         if (tid == 255 && E == 1024) c[E] = base;
     }
-    __syncthreads();
+    lds_barrier();
 }
 
 // Writes the places of `slots` choices that start at slot0, in turns of one
-// choice a thread. first[e] (LDS): the next place within expert e; cnt: LDS of
-// NT / 64 times E words. Within a wave, the lanes of one expert find each
-// other by a vote per bit of the index; the counts of the waves before give
-// the rest of the rank.
+// choice a thread; id: the thread's first choice (-1: none). first[e] (LDS):
+// the next place within expert e; cnt: LDS of NT / 64 times E words. Within a
+// wave, the lanes of one expert find each other by a vote per bit of the
+// index; the counts of the waves before give the rest of the rank.
 template <int NT>
-__device__ __forceinline__ void place(const int32_t* ids, int64_t slots, int64_t slot0, int32_t* first, int32_t* cnt,
+__device__ __forceinline__ void place(const int32_t* ids, int id, int slots, int slot0, int32_t* first, int32_t* cnt,
                                       int E, uint32_t k, int32_t* rows, int32_t* pos, int tid) {
+    constexpr int W = NT / 64;
     const int lane = tid & 63, wave = tid >> 6;
     const int bits = 32 - __builtin_clz((uint32_t)(E - 1) | 1u);
-    for (int64_t s0 = 0; s0 < slots; s0 += NT) {
-        for (int i = tid; i < NT / 64 * E; i += NT) cnt[i] = 0;
-        __syncthreads();
-        const int64_t s = s0 + tid;
-        const int id = s < slots ? ids[s] : -1;
+    for (int s0 = 0; s0 < slots; s0 += NT) {
+        const int s = s0 + tid;
+        const int next = slots - s > NT ? ids[s + NT] : -1;
+        for (int i = tid; i < W * E; i += NT) cnt[i] = 0;
         uint64_t same = __ballot(id >= 0);
         for (int b = 0; b < bits; ++b) {
-            const uint64_t ones = __ballot((id >> b) & 1);
-            same &= ((id >> b) & 1) ? ones : ~ones;
+            const bool one = (id >> b) & 1;
+            const uint64_t ones = __ballot(one);
+            same &= one ? ones : ~ones;
         }
         const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+        lds_barrier();
         if (id >= 0 && rank == 0) cnt[wave * E + id] = __builtin_popcountll(same);
-        __syncthreads();
+        lds_barrier();
         for (int e = tid; e < E; e += NT) {
-            int at = first[e];
+            int c[W], at = first[e];
 #pragma unroll
-            for (int w = 0; w < NT / 64; ++w) {
-                const int c = cnt[w * E + e];
+            for (int w = 0; w < W; ++w) c[w] = cnt[w * E + e];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
                 cnt[w * E + e] = at;
-                at += c;
+                at += c[w];
             }
             first[e] = at;
         }
-        __syncthreads();
+        lds_barrier();
         if (s < slots) {
             int at = -1;
             if (id >= 0) {
                 at = cnt[wave * E + id] + rank;
-                rows[at] = (int32_t)((uint64_t)(slot0 + s) / k);
+                rows[at] = (int32_t)((uint32_t)(slot0 + s) / k);     // T * k < 2^31
             }
             pos[slot0 + s] = at;
         }
-        __syncthreads();
+        id = next;
+        lds_barrier();
     }
 }
 
@@ -388,7 +405,7 @@ route_kernel(RouteProblem p, int rows_per_block) {
             float a = 0.0f;
 #pragma unroll
             for (int w = 0; w < W; ++w) a += psum[w][e];
-            ws.hist[(int64_t)blockIdx.x * E + e] = hist[e];
+            ws.hist[(int64_t)blockIdx.x * E + e] = (uint16_t)hist[e];
             ws.psum[(int64_t)blockIdx.x * E + e] = a;
         }
         if (tid == 0) ws.live[blockIdx.x] = n;
@@ -417,81 +434,122 @@ route_kernel(RouteProblem p, int rows_per_block) {
         const int slots = (int)p.T * k;
         for (int i = hist[E] + tid; i < slots; i += NT) p.out.rows[i] = -1;
         __syncthreads();
-        place<NT>(p.out.ids, slots, 0, hist, cnt, E, p.k, p.out.rows, p.out.pos, tid);
+        place<NT>(p.out.ids, tid < slots ? p.out.ids[tid] : -1, slots, 0, hist, cnt, E, p.k, p.out.rows, p.out.pos, tid);
     }
 }
 
-// Workgroup b < blocks: the places of the rows that workgroup b of the first
-// kernel owned. The last workgroup: counts, offsets and statistics.
 constexpr int PLACE_NT = 1024;
-constexpr int STRETCHES = 16;
-__global__ void __launch_bounds__(PLACE_NT)
+constexpr int PARTS = 4096;                      // partial sums of experts in LDS
+
+// Over the first kernel's workgroups: off[e], the counts of expert e; for
+// b >= 0, before[e], those of the workgroups before b; for b < 0, mean[e], the
+// sums of probabilities.
+template <int N>
+__device__ __forceinline__ void sum_blocks(const RouteWs& ws, int E, int blocks, int b, int32_t* cnt,
+                                           int32_t* off, int32_t* before, float* mean, int tid) {
+    typedef int32_t Ints __attribute__((ext_vector_type(N)));
+    typedef float Floats __attribute__((ext_vector_type(N)));
+    typedef uint16_t Shorts __attribute__((ext_vector_type(N)));
+    const int groups = (E + N - 1) / N;          // of N experts
+    int wide = 16;                               // threads side by side: a power of two that holds them
+    while (wide < groups) wide *= 2;
+    const int segs = min(PLACE_NT / wide, PARTS / (wide * N)), g = tid & (wide - 1), seg = tid / wide;
+    const bool in = g < groups && seg < segs;
+    Ints all = {}, mine = {};
+    Floats a = {};
+    if (in) {
+        const uint16_t* h = ws.hist + g * N;
+        const float* f = ws.psum + g * N;
+        // Batches of loads in flight together (past the end the batch's first
+        // again). For b < 0 half of the threads add the counts, half the
+        // probabilities; a single part does both.
+        const int part = b < 0 && segs > 1 ? segs / 2 : segs;
+        const bool counts = seg < part, probs = b < 0 && (seg >= part || segs == 1);
+        constexpr int BATCH = 8;
+        for (int q0 = seg; counts && q0 < blocks; q0 += BATCH * part) {
+            Shorts c[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                c[u] = *reinterpret_cast<const Shorts*>(h + (int64_t)(q0 + u * part < blocks ? q0 + u * part : q0) * E);
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int q = q0 + u * part;
+                const Ints x = __builtin_convertvector(c[u], Ints);
+                all += q < blocks ? x : Ints{};
+                mine += q < b ? x : Ints{};
+            }
+        }
+        for (int q0 = seg >= part ? seg - part : seg; probs && q0 < blocks; q0 += BATCH * part) {
+            Floats d[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                d[u] = *reinterpret_cast<const Floats*>(f + (int64_t)(q0 + u * part < blocks ? q0 + u * part : q0) * E);
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) a += q0 + u * part < blocks ? d[u] : Floats{};
+        }
+        *reinterpret_cast<Ints*>(cnt + seg * wide * N + g * N) = all;
+        *reinterpret_cast<Ints*>(cnt + PARTS + seg * wide * N + g * N) = mine;
+        *reinterpret_cast<Ints*>(cnt + 2 * PARTS + seg * wide * N + g * N) = __builtin_bit_cast(Ints, a);
+    }
+    lds_barrier();
+    for (int e = tid; e < E; e += PLACE_NT) {
+        int x = 0, y = 0;
+        float z = 0.0f;
+        // four parts' loads at a time; past the last part, that one again, times nothing
+        for (int q0 = 0; q0 < segs; q0 += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool is = q0 + u < segs;
+                const int at = min(q0 + u, segs - 1) * wide * N + e;
+                x += is ? cnt[at] : 0;
+                y += is ? cnt[PARTS + at] : 0;
+                z += is ? __builtin_bit_cast(float, cnt[2 * PARTS + at]) : 0.0f;
+            }
+        }
+        off[e] = x;
+        before[e] = y;
+        mean[e] = z;
+    }
+    lds_barrier();
+}
+
+// Workgroup 0: counts, offsets and statistics. Workgroup b + 1: the places of
+// the rows that workgroup b of the first kernel owned. Two of them have to fit
+// one compute unit (80 KB of LDS, 64 registers): of 257 that fill one each, the
+// last would start when another has ended.
+__global__ void __launch_bounds__(PLACE_NT, 8)
 route_place_kernel(RouteProblem p, int rows_per_block, int blocks) {
     __shared__ int32_t off[kMaxExperts + 1];
     __shared__ int32_t before[kMaxExperts];
     __shared__ float mean[kMaxExperts];
-    __shared__ int32_t cnt[PLACE_NT / 64 * kMaxExperts];
-    __shared__ float fsum[STRETCHES * 64];
+    __shared__ __attribute__((aligned(16))) int32_t cnt[PLACE_NT / 64 * kMaxExperts];
     __shared__ int32_t live;
-    const int tid = threadIdx.x, E = (int)p.E, b = (int)blockIdx.x;
+    const int tid = threadIdx.x, E = (int)p.E, b = (int)blockIdx.x - 1;
     const RouteWs ws = split_ws(p.ws, (uint64_t)blocks, p.E);
-    // Sums over the workgroups of the first kernel: thread (expert, stretch of
-    // workgroups), 64 experts and 16 stretches at a time; the stretches'
-    // sums meet in LDS and are added in order.
-    const int el = tid & 63, seg = tid >> 6;
-    const int per = (blocks + STRETCHES - 1) / STRETCHES, b0 = min(seg * per, blocks), b1 = min(b0 + per, blocks);
+    // Sums over the workgroups of the first kernel. A thread takes four experts
+    // (one, where rows are not whole 16-byte loads) and every `segs`-th
+    // workgroup, with its loads in flight at once; the partial sums meet in
+    // LDS and are added in order.
     if (tid == 0) live = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + el;
-        int all = 0, mine = 0;
-        float a = 0.0f;
-        if (e < E) {
-            if (b < blocks) {
-#pragma unroll 8
-                for (int q = b0; q < b1; ++q) {
-                    const int c = ws.hist[(int64_t)q * E + e];
-                    all += c;
-                    mine += q < b ? c : 0;
-                }
-            } else {
-#pragma unroll 8
-                for (int q = b0; q < b1; ++q) {
-                    all += ws.hist[(int64_t)q * E + e];
-                    a += ws.psum[(int64_t)q * E + e];
-                }
-            }
-        }
-        cnt[seg * 64 + el] = all;
-        cnt[(STRETCHES + seg) * 64 + el] = mine;
-        fsum[seg * 64 + el] = a;
-        __syncthreads();
-        if (tid < 64 && e < E) {
-            all = mine = 0;
-            a = 0.0f;
-#pragma unroll
-            for (int q = 0; q < STRETCHES; ++q) {
-                all += cnt[q * 64 + el];
-                mine += cnt[(STRETCHES + q) * 64 + el];
-                a += fsum[q * 64 + el];
-            }
-            off[e] = all;
-            before[e] = mine;
-            mean[e] = a;
-        }
-        __syncthreads();
-    }
-    if (b == blocks) {
-        int n = 0;
-        for (int q = tid; q < blocks; q += PLACE_NT) n += ws.live[q];
+    const int64_t t0 = (int64_t)max(b, 0) * rows_per_block, t1 = min(t0 + rows_per_block, (int64_t)p.T);
+    const int slots = b >= 0 ? (int)(t1 - t0) * (int)p.k : 0, slot0 = (int)(t0 * p.k);
+    const int id = tid < slots ? p.out.ids[slot0 + tid] : -1;    // in flight meanwhile
+    int n = b < 0 && tid < blocks ? ws.live[tid] : 0;
+    if (E % 4 == 0)
+        sum_blocks<4>(ws, E, blocks, b, cnt, off, before, mean, tid);
+    else
+        sum_blocks<1>(ws, E, blocks, b, cnt, off, before, mean, tid);
+    if (b < 0) {
+        for (int q = tid + PLACE_NT; q < blocks; q += PLACE_NT) n += ws.live[q];
         if (n != 0) atomicAdd(&live, n);
-        __syncthreads();
+        lds_barrier();
         n = live;
         for (int e = tid; e < E; e += PLACE_NT) {
             mean[e] = n > 0 ? mean[e] / (float)n : 0.0f;
             p.out.mean_probs[e] = mean[e];
             p.out.counts[e] = off[e];
         }
-        __syncthreads();
+        lds_barrier();
         if (tid < 64) {
             const float l = balance(off, mean, E, p.k, n, tid);
             if (tid == 0) {
@@ -499,7 +557,7 @@ route_place_kernel(RouteProblem p, int rows_per_block, int blocks) {
                 *p.out.n_valid = n;
             }
         }
-        __syncthreads();
+        lds_barrier();
         scan_counts(off, E, tid);
         for (int e = tid; e <= E; e += PLACE_NT) p.out.offsets[e] = off[e];
         return;
@@ -510,8 +568,7 @@ route_place_kernel(RouteProblem p, int rows_per_block, int blocks) {
     for (int64_t i = off[E] + (int64_t)b * PLACE_NT + tid; i < all; i += (int64_t)blocks * PLACE_NT) p.out.rows[i] = -1;
     for (int e = tid; e < E; e += PLACE_NT) off[e] += before[e];
     __syncthreads();
-    const int64_t t0 = (int64_t)b * rows_per_block, t1 = min(t0 + rows_per_block, (int64_t)p.T);
-    place<PLACE_NT>(p.out.ids + t0 * p.k, (t1 - t0) * p.k, t0 * p.k, off, cnt, E, p.k, p.out.rows, p.out.pos, tid);
+    place<PLACE_NT>(p.out.ids + slot0, id, slots, slot0, off, cnt, E, p.k, p.out.rows, p.out.pos, tid);
 }
 
 // Gradient: the row's probabilities again from its logits, the loss's part in
@@ -530,32 +587,27 @@ route_backward_kernel(RouteBackwardProblem p) {
     const float scale = p.dloss != nullptr && n > 0.0f ? *p.dloss * (float)E / ((float)k * n) / n : 0.0f;
     float c[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) c[i] = e0 + i < E ? scale * (float)p.counts[e0 + i] : 0.0f;
+    for (int i = 0; i < VPL; ++i) c[i] = scale * (float)p.counts[min(e0 + i, E - 1)];     // past E: times a zero
     float* const row = extra[tok];
 #pragma unroll
     for (int i = 0; i < PITCH; i += 4) *reinterpret_cast<f32x4*>(row + gl * PITCH + i) = f32x4{};
-    for (int64_t tb = (int64_t)blockIdx.x * TOK; tb < (int64_t)p.T; tb += (int64_t)gridDim.x * TOK) {
-        const int64_t t = tb + tok;
-        if (t >= (int64_t)p.T) break;            // whole groups leave together
-        // a live row has a first choice
-        const bool live = p.ids[t * k] >= 0;
+    for (int64_t t = (int64_t)blockIdx.x * TOK + tok; t < (int64_t)p.T; t += (int64_t)gridDim.x * TOK) {
+        // whole groups leave the loop together; all of a row's loads go out at once
         float v[VPL], top = NEG_INF;
-        if (live) {
-            load_logits<F32, VPL, VEC>(p.logits, t, E, e0, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) v[i] = NEG_INF;
-        }
+        load_logits<F32, VPL, VEC>(p.logits, t, E, e0, v);
+        const int first = p.ids[t * k];          // a live row has a first choice
         int id = -1;
         float w = 0.0f, g = 0.0f;
-        if (live && gl < k && p.dweights != nullptr) {
+        if (gl < k && p.dweights != nullptr) {
             id = p.ids[t * k + gl];
-            if (id >= 0 && id < E) {
-                w = p.weights[t * k + gl];
-                g = w * p.dweights[t * k + gl];
-            } else {
-                id = -1;
-            }
+            w = p.weights[t * k + gl];
+            g = w * p.dweights[t * k + gl];
+        }
+        const bool live = first >= 0;
+        if (id < 0 || id >= E || !live) id = -1, w = 0.0f, g = 0.0f;
+        if (!__all(live)) {                      // what a row that is not live holds is not used
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) v[i] = live ? v[i] : NEG_INF;
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) top = fmaxf(top, v[i]);
@@ -656,7 +708,7 @@ hipError_t launch_moe_route(const RouteProblem& p, hipStream_t stream) {
             constexpr bool F = decltype(f32)::value;
             if (one) route_kernel<F, G, V, VEC, 512, true><<<1, 512, 0, stream>>>(p, rows);
             else if (wide) route_kernel<F, G, V, VEC, 1024, false><<<blocks, 1024, 0, stream>>>(p, rows);
-            else route_kernel<F, G, V, VEC, 256, false><<<blocks, 256, 0, stream>>>(p, rows);
+            else route_kernel<F, G, V, VEC, 512, false><<<blocks, 512, 0, stream>>>(p, rows);
         };
         if (p.type == BG_F32) run(std::true_type{});
         else run(std::false_type{});
@@ -672,7 +724,7 @@ hipError_t launch_moe_route_backward(const RouteBackwardProblem& p, hipStream_t 
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
         constexpr bool VEC = decltype(vec)::value;
         const uint32_t passes = (p.T + 256 / G - 1) / (256 / G);
-        const uint32_t blocks = passes < 2048 ? passes : 2048;
+        const uint32_t blocks = passes < 1024 ? passes : 1024;
         if (p.type == BG_F32) route_backward_kernel<true, G, V, VEC><<<blocks, 256, 0, stream>>>(p);
         else route_backward_kernel<false, G, V, VEC><<<blocks, 256, 0, stream>>>(p);
     });

@@ -56,7 +56,7 @@ hipError_t launch_moe_route(const RouteProblem& p, hipStream_t) {
     // every workgroup owns a row range, and the ranges cover the batch
     const uint64_t rows = route_rows_per_block(p.T), blocks = route_blocks(p.T);
     CHECK(p.T <= kRouteOneBlock || (rows * blocks >= p.T && rows * (blocks - 1) < p.T));
-    CHECK(rows % 16 == 0 && blocks <= 256);
+    CHECK(rows % 32 == 0 && rows < 65536 && (blocks <= 256 || p.T > 256 * 65000u));
     ++g_launches;
     return hipSuccess;
 }
@@ -97,7 +97,7 @@ int main() {
                        at<int32_t>(0x600000000), at<int32_t>(0x700000000), at<int32_t>(0x800000000),
                        at<float>(0x900000000),   at<float>(0xA00000000),   at<int32_t>(0xB00000000)};
     void* ws = at<void>(0xC00000000);
-    for (uint32_t T : {0u, 1u, 64u, 65u, 100u, 8192u, 8193u, 4510u, 65536u, 1000003u, 100000000u}) {
+    for (uint32_t T : {0u, 1u, 64u, 65u, 100u, 16384u, 16385u, 4510u, 65536u, 1000003u, 100000000u}) {
         const size_t need = moe_route_workspace_bytes(T, 256);
         CHECK((need == 0) == (T <= bg::kRouteOneBlock));
         CHECK(moe_route(A, BG_BF16, nullptr, &out, ws, need, T, 256, 8, 1, nullptr) ==
