@@ -878,7 +878,7 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
         int bm, bn;
         double fixed, alone, paired;   // paired 0: one workgroup fills a compute unit's LDS
     };
-    static constexpr Tile tiles[] = {{256, 256, 4.0, 2.15, 0},    {256, 128, 2.1, 1.19, 0},   {128, 128, 2.0, 0.68, 1.3},
+    static constexpr Tile tiles[] = {{256, 256, 4.0, 2.15, 0},    {256, 128, 2.1, 1.14, 0},   {128, 128, 2.0, 0.61, 1.3},
                                      {128, 64, 2.5, 0.45, 0.77}, {64, 64, 1.5, 0.31, 0.54}, {32, 64, 1.5, 0.23, 0.4}};
     const double steps = (p.K + 255) / 256;
     int best = 0;
@@ -898,8 +898,12 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
     }
     switch (best) {
         case 0: return launch_tile<256, 256, 2, 4, 2, false, 2, 2>(p, stream);
-        case 1: return launch_tile<256, 128, 4, 2, 2, false>(p, stream);
-        case 2: return launch_tile<128, 128, 4, 2, 2, false, 2, 2>(p, stream);
+        case 1: return launch_tile<256, 128, 4, 2, 3, false>(p, stream);
+        case 2:
+            // one to a compute unit: LDS for four stages (512 x 7168 x 16384: 41 us, 50 with two)
+            if ((uint64_t)((p.M + 127) / 128) * ((p.N + 127) / 128) <= (uint64_t)p.cus)
+                return launch_tile<128, 128, 4, 2, 4, false, 2, 2>(p, stream);
+            return launch_tile<128, 128, 4, 2, 2, false, 2, 2>(p, stream);
         case 3: return launch_tile<128, 64, 2, 2, 3, false>(p, stream);
         case 4: return launch_tile<64, 64, 2, 2, 4, false>(p, stream);
     }

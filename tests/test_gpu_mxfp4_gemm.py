@@ -43,6 +43,25 @@ def test_product_at_full_size(m, n, k):
     assert_bits_equal(got[rows], exact_bits(a[rows], ea[rows], b, eb), f"full {m}x{n}x{k}")
 
 
+# Every tile of the dense product with K below 512, of whole steps, and of any
+# other length; few rows with K that ends inside a turn of the eight waves.
+TILES = [(9, 500, 4128), (16, 60, 8192), (100, 4100, 32), (100, 4099, 480), (2812, 1430, 288), (100, 9000, 4096), (100, 9000, 4128),
+         (129, 12000, 512), (129, 12001, 544), (129, 12002, 160), (2000, 4100, 512), (2001, 4100, 480), (300, 12000, 1056),
+         (300, 12004, 352), (3000, 4100, 2080), (3001, 4097, 416)]
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_product_of_every_tile(m, n, k):
+    """Exact sums as above; every row of few columns and every column of few rows."""
+    print(f"mxfp4 tiles {m}x{n}x{k}", flush=True)
+    a, b = synthetic.fp4_packed(m, k, 21, 0), synthetic.fp4_packed(n, k, 21, 1)
+    ea, eb = e8m0(m, k // 32, 127, 128, 21, 4), e8m0(n, k // 32, 127, 128, 21, 5)
+    got = bits_of(bg.gemm_mxfp4(dev(a), dev(ea), dev(b), dev(eb)))
+    rows, cols = synthetic.sample_rows(m, min(m, 64), 21), synthetic.sample_rows(n, min(n, 64), 22)
+    assert_bits_equal(got[rows], exact_bits(a[rows], ea[rows], b, eb), f"rows of {m}x{n}x{k}")
+    assert_bits_equal(got[:, cols], exact_bits(a, ea, b[cols], eb[cols]), f"columns of {m}x{n}x{k}")
+
+
 def test_scales_over_the_whole_range():
     """Scale bytes from 0 to 254: products from 2^-254 (zero in FP32) past FP32's largest."""
     a, _ = operand(40, 256, 11, 0)
