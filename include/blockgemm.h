@@ -446,7 +446,10 @@ bg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, void* ou
  * unspecified but fixed by the shape: repeated calls return identical bits.
  *
  *  K % 32 == 0 and K <= 2^24 (BG_ERR_SHAPE otherwise).
- *  A: [M, K/2], SFA: [M, K/32], B: [N, K/2], SFB: [N, K/32] bytes, read.
+ *  A: [M, K/2], SFA: [M, K/32], B: [N, K/2], SFB: [N, K/32] bytes, read. Scales
+ *     are read in aligned four-byte words: where an array of them ends inside
+ *     a word, the up to three bytes behind it in that word are read too (never
+ *     another word, so never another page) and not used.
  *  C: [M, N] BF16, written; must not overlap an input (BG_ERR_ALIAS).
  */
 bg_status gemm_mxfp4(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB, uint16_t* C,
@@ -495,8 +498,8 @@ bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t
  * Choices that do not exist (rows that are not live, or with fewer than k
  * logits above -infinity) have ids -1, weights 0, pos -1. With n = 0, loss and
  * mean_probs are 0. A live row with a NaN or a +infinity has NaN weights, and
- * makes mean_probs and loss NaN; its ids and places stay valid. Logits of rows
- * that valid leaves out are not read. Sums over rows are added in a fixed
+ * makes mean_probs and loss NaN; its ids and places stay valid. What the logits
+ * of rows hold that valid leaves out changes nothing. Sums over rows are added in a fixed
  * order: repeated calls return identical bits.
  *
  *  logits: [T, E] of logits_type, read.  valid: T bytes or NULL.
