@@ -72,3 +72,45 @@ def test_quantised_linear_close_to_the_unquantised_product():
     ref = f64(av) @ f64(bv).T
     tol = 2.0 ** -7 * np.abs(ref) + 4 * (k + 1) * U * size
     assert (np.abs(f64(got) - f64(dense)) <= tol).all()
+
+
+@pytest.mark.parametrize("t", [1, 200])
+def test_layer_captured_and_replayed(t):
+    """The whole chain in one graph, replayed over changing inputs with eager
+    calls between, gives the eager bits; places behind the last keep what the
+    output held."""
+    e, k, d, n = 16, 4, 512, 264
+    w, ws = bg.mxfp4_quantize(torch.randn(e * n, d, device="cuda").bfloat16())
+    w, ws = w.view(e, n, -1), ws.view(e, n, -1)
+    router = torch.randn(e, d, device="cuda").bfloat16()
+    x, valid = torch.empty(t, d, device="cuda", dtype=torch.bfloat16), torch.empty(t, device="cuda", dtype=torch.bool)
+    y = torch.empty(t * k, n, device="cuda", dtype=torch.bfloat16)
+    dw, dl = torch.randn(t, k, device="cuda"), torch.tensor(0.3, device="cuda")
+
+    def layer():
+        logits = bg.gemm_bf16_ordered_f32(x, router)
+        r = bg.moe_route(logits, k, valid=valid)
+        a, sa = bg.mxfp4_quantize(x, rows=r.rows)
+        bg.gemm_mxfp4_grouped(a, sa, w, ws, r.offsets, out=y)
+        return *r[:9], a, sa, bg.moe_route_backward(logits, r, dw, dl)
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x.copy_(torch.randn(t, d, device="cuda", generator=g))
+        valid.copy_(torch.rand(t, device="cuda", generator=g) < (0.7 if seed % 2 else 2.0))
+        y.fill_(5.0)
+
+    fill(0)
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = layer()
+    for seed in range(5):
+        fill(seed)
+        want = [v.clone() for v in (*layer(), y)]
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*held, y), want)), seed
+        assert (y[int(held[3][-1]):] == 5.0).all()

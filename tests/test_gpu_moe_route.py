@@ -237,3 +237,32 @@ def test_large_batch_counts_and_places():
     assert torch.equal(r.pos.flatten().long()[by], torch.arange(t * k, device="cuda"))
     p = torch.softmax(x.double(), 1).mean(0)
     assert ((r.mean_probs.double() - p).abs() <= 2.0 ** -24 * (e + 2 * 20 + 16 + 300) * p).all()
+
+
+def test_more_rows_than_256_workgroups_count():
+    """Workgroups count at most 65472 rows each (16 bits): a batch of 260 of
+    them, an odd number of experts, a mask that starts at an odd address."""
+    t, e = 17000000, 3
+    x = torch.randn(t, e, device="cuda").bfloat16()
+    valid = (torch.rand(t + 1, device="cuda") < 0.9)[1:]
+    r = bg.moe_route(x, 1, valid=valid)
+    ids = torch.where(valid, torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, 0], -1)
+    assert torch.equal(r.ids[:, 0].long(), ids)
+    live = valid.nonzero().flatten()
+    by = live[torch.sort(ids[live], stable=True).indices]
+    n = int(by.numel())
+    assert int(r.n_valid) == n
+    assert torch.equal(r.counts.long(), torch.bincount(ids[live], minlength=e))
+    assert torch.equal(r.rows[:n].long(), by) and (r.rows[n:] == -1).all()
+    assert torch.equal(r.pos[by, 0].long(), torch.arange(n, device="cuda")) and (r.pos[~valid] == -1).all()
+    p = torch.softmax(x[valid].double(), 1).mean(0)
+    # 65472 rows of a workgroup 64 at a time: 1023 additions in a lane, 4 over lanes, 16 over waves, 260 over workgroups
+    assert ((r.mean_probs.double() - p).abs() <= 2.0 ** -24 * (e + 2 * 12 + 16 + 1400) * p).all()
+    d = bg.moe_route_backward(x, r, dloss=torch.tensor(1e6, device="cuda"))
+    assert (d[~valid] == 0).all()
+    c = 1e6 * e * r.counts.double() / float(n) ** 2
+    at = torch.cat((live[:1000], live[-1000:]))
+    pr = torch.softmax(x[at].double(), 1)
+    want = pr * (c - (pr * c).sum(1, keepdim=True))
+    size = pr * (c + (pr * c).sum(1, keepdim=True))
+    assert ((d[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -24 * 3 * (e + 2 * 12 + 32) * size).all()
