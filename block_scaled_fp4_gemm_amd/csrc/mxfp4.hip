@@ -155,7 +155,8 @@ mxfp4_quantize_kernel(MxQuantProblem p, uint32_t segs, uint32_t per_seg, uint32_
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: four code bytes, eight values, per lane and step.
+// Reading back: four code bytes, eight values, per lane and step; 5120 x 11008
+// to BF16 in 21.8 us (6.6 TB/s).
 // ---------------------------------------------------------------------------
 
 // 2^(s - 127) as FP32 (s = 0: the subnormal 2^-127; s = 255: NaN).
@@ -293,7 +294,6 @@ __device__ __forceinline__ void interleave() {
 }
 
 constexpr int STEP = 8;                         // blocks per K step: 128 bytes of every row, one cache line
-constexpr int PAIR = 2 * STEP;                  // scales are staged for two steps at once: 16 bytes of every row
 
 // Swizzled 16-byte slot of block c in row `row` of a staged tile of eight
 // blocks a row: the rows that the lanes of one 16-byte LDS read touch spread
@@ -349,33 +349,44 @@ struct MxStager {
 
 // How the scales of a tile's rows come to LDS, by K alone:
 enum ScalePath : int {
-    WHOLE = 0,     // K % 256 == 0, K >= 512: rows of whole steps, four-byte aligned
+    WHOLE = 0,     // K % 256 == 0, at least a group of steps: rows four-byte aligned
     SHIFTED = 1,   // any other K >= 512: rows start at any byte
     SHORT = 2,     // K < 512
 };
-constexpr ScalePath scale_path(uint32_t K) { return K < PAIR * 32 ? SHORT : K % (STEP * 32) == 0 ? WHOLE : SHIFTED; }
+template <int Q>
+constexpr ScalePath scale_path(uint32_t K) {
+    return K < 512 ? SHORT : K % (STEP * 32) == 0 && K >= Q * STEP * 32 ? WHOLE : SHIFTED;
+}
 
-// Scales of the BM rows of A and the BN rows of B of a tile, a pair of steps
-// at a time as [row][16] bytes in LDS, by direct loads, one row a lane. A row
-// of 8 bytes a step costs a cache request for every 8 bytes, as many as all
-// its codes; two steps at once halve that (64 x 64 tiles, 128 x 7168 x 16384:
-// 27 us before, 22 us after). A last pair that ends past the row starts
-// earlier, so that it ends with it.
-// SHIFTED: the loads start at the four-byte word that holds a row's first
-// scale, and one more word a row ([row][4] behind the others) holds the up to
-// three scales that the shift pushes out; a lane joins its four out of two
-// words. (The same through registers and LDS writes: 4096 x 4096 x 8224 in 92
-// us.) The last word may reach up to three bytes past the last scale of the
+// Scales of the BM rows of A and the BN rows of B of a tile, a group of Q steps
+// (two or four) at a time as [row][GROUP] bytes in LDS, by direct loads of 16
+// bytes a lane. What a load costs is the cache lines it touches: a step's 8
+// bytes of scales are one, as many as its 128 bytes of codes, so groups cut
+// the lines a row and step touches from 2 to 1.5 (pairs) or 1.25 (fours):
+// 64 x 64 tiles, 128 x 7168 x 16384, 27 us step by step, 20.8 in pairs, 19.2 in
+// fours; 128 x 128 tiles, 4096 x 4096 x 8192, 88.8 us in pairs and 82.4 in
+// fours; the experts' tiles of 32 x 128, 16 x 8 of 256 of 2048 x 2048, 41.0 and
+// 39.7. Fours stay out where their buffers cost a stage or a second workgroup
+// (256 x 128 tiles 78.9 us in pairs with three stages, 80.0 in fours with two),
+// registers (256 x 256: 72.5 and 76.2) or, with 32 x 64, nothing is gained.
+// A last group that ends past the row starts earlier, so that it ends with it.
+// SHIFTED (pairs): the loads start at the four-byte word that holds a row's
+// first scale, and one more word a row ([row][4] behind the others) holds the
+// up to three scales that the shift pushes out; a lane joins its four out of
+// two words. (The same through registers and LDS writes: 4096 x 4096 x 8224 in
+// 92 us.) The last word may reach up to three bytes past the last scale of the
 // whole operand: never past the word that holds it.
 // SHORT: through registers, a step at a time, zero past the row's end.
-template <int BM, int BN, int NW, int PATH>
+template <int BM, int BN, int NW, int PATH, int Q>
 struct ScaleStager {
-    // a stretch of 64 rows belongs to one operand: 32 rows of A take one of their own
-    static constexpr int PAD = BM < 64 ? 64 : BM;
-    static constexpr int SEGS = (PAD + BN) / 64, SPER = (SEGS + NW - 1) / NW;
+    static constexpr int GROUP = Q * STEP, LANES = GROUP / 16, RPL = 64 / LANES;     // lanes per row, rows per load
+    // a load's rows belong to one operand: fewer rows of A take one of their own
+    static constexpr int PAD = BM < RPL ? RPL : BM;
+    static constexpr int SEGS = (PAD + BN) / RPL, SPER = (SEGS + NW - 1) / NW;
     static constexpr int PER = PATH == WHOLE ? SPER : PATH == SHIFTED ? 2 * SPER : 0;
-    static_assert(PAD % 64 == 0 && BN % 64 == 0, "whole stretches");
-    static constexpr int REST = (PAD + BN) * PAIR;                 // where the fifth words start
+    static_assert(PAD % RPL == 0 && BN % RPL == 0, "whole loads");
+    static_assert(LANES == 1 || (LANES == 2 && PATH == WHOLE), "pairs, or fours of whole steps");
+    static constexpr int REST = (PAD + BN) * GROUP;                // where the fifth words start
     static constexpr int BYTES = REST + (PATH == SHIFTED ? (PAD + BN) * 4 : 0);
     static constexpr int WORDS = (BM + BN) * 2, WPER = (WORDS + NW * 64 - 1) / (NW * 64);
     uint32_t off[PATH == SHORT ? WPER : SPER], lim[SPER];
@@ -392,12 +403,12 @@ struct ScaleStager {
         if constexpr (PATH != SHORT) {
 #pragma unroll
             for (int j = 0; j < SPER; ++j) {
-                const int r = seg(wave, j) * 64;
+                const int r = seg(wave, j) * RPL, at = lane / LANES;
                 const bool is_a = r < PAD;
                 const uint8_t* first = is_a ? a : b;
                 const uint32_t odd = PATH == SHIFTED ? (uint32_t)(reinterpret_cast<uintptr_t>(first) & 3) : 0;
                 rsrc[j] = resource(first - odd);
-                off[j] = odd + (uint32_t)(is_a ? min(r + lane, last_a) : min(r - PAD + lane, last_b)) * blocks;
+                off[j] = odd + (uint32_t)(is_a ? min(r + at, last_a) : min(r - PAD + at, last_b)) * blocks + lane % LANES * 16;
                 // offset of the word that holds the operand's last scale
                 lim[j] = (uint32_t)min(odd + (is_a ? left_a : left_b) - 1, (int64_t)0x7FFFFFFF) & ~3u;
             }
@@ -411,10 +422,10 @@ struct ScaleStager {
             }
         }
     }
-    // first block of the pair that a step's scales are staged with
-    __device__ __forceinline__ static uint32_t pair_start(int step, uint32_t blocks) {
-        const uint32_t c = (uint32_t)(step / 2) * PAIR;
-        return PATH == SHORT ? c : min(c, blocks - PAIR);
+    // first block of the group that a step's scales are staged with
+    __device__ __forceinline__ static uint32_t group_start(int step, uint32_t blocks) {
+        const uint32_t c = (uint32_t)step / Q * GROUP;
+        return PATH == SHORT ? c : min(c, blocks - GROUP);
     }
     __device__ __forceinline__ void issue(uint32_t c0, uint8_t* lds, int wave) const {
         const uint32_t c = PATH == SHIFTED ? c0 & ~3u : c0;
@@ -450,24 +461,24 @@ struct ScaleStager {
             const int w = min((j * NW + wave) * 64 + lane, WORDS - 1);
             const uint32_t c = word_block(step, w), past = c - min(c, max(blocks, 4u) - 4);
             const int row = w / 2 + (w / 2 < BM ? 0 : PAD - BM);
-            *reinterpret_cast<uint32_t*>(lds + row * PAIR + (step & 1) * STEP + (w & 1) * 4) =
+            *reinterpret_cast<uint32_t*>(lds + row * GROUP + step % Q * STEP + (w & 1) * 4) =
                 past < 4 ? reg[j] >> (8 * past) : 0u;
         }
     }
-    // Into v: the four scales from byte `at` of a pair on (the step's part of
+    // Into v: the four scales from byte `at` of a group on (the step's part of
     // it and the lane's half) of the N rows row, row + 32, ..., whose first
     // scale lies `odd` bytes into its word.
     template <int N>
     __device__ __forceinline__ static void read(const uint8_t* lds, int row, uint32_t at, uint32_t odd, int (&v)[N]) {
         if constexpr (PATH != SHIFTED) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const int*>(lds + row * PAIR + at + 32 * PAIR * i);
+            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const int*>(lds + row * GROUP + at + 32 * GROUP * i);
         } else {
             const uint32_t o = at + odd, w = o >> 2;
             const bool l4 = w < 4, h4 = w < 3;
-            const uint8_t* lo = lds + (l4 ? row * PAIR + w * 4 : REST + row * 4);
-            const uint8_t* hi = lds + (h4 ? row * PAIR + w * 4 + 4 : REST + row * 4);
-            const int ls = l4 ? 32 * PAIR : 128, hs = h4 ? 32 * PAIR : 128;
+            const uint8_t* lo = lds + (l4 ? row * GROUP + w * 4 : REST + row * 4);
+            const uint8_t* hi = lds + (h4 ? row * GROUP + w * 4 + 4 : REST + row * 4);
+            const int ls = l4 ? 32 * GROUP : 128, hs = h4 ? 32 * GROUP : 128;
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 v[i] = (int)__builtin_amdgcn_alignbyte(*reinterpret_cast<const uint32_t*>(hi + hs * i),
@@ -483,32 +494,39 @@ struct ScaleStager {
 // needs for a step are one aligned word, and the instruction picks byte s of
 // it: no vector instruction touches codes or scales between LDS and the matrix
 // cores. The steps' codes go through a ring of STAGES buffers in LDS, the
-// scales through buffers of a pair of steps, filled by direct loads.
+// scales through buffers of a group of Q steps, filled by direct loads.
 // Where K ends inside a step, A's blocks past the end and all scales there
 // become zero in registers.
 // The matrix instruction takes B first, so a lane ends up with four
 // consecutive columns of one row of C.
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int PATH>
+//
+// Bound by staging, about 50 bytes per ns and compute unit from L2 to LDS with
+// every tile shape, and by power: 4096 x 4096 x 8192 in 76 us (3.6 PFLOP/s),
+// 5120 x 11008 x 2048 in 85 us (2.7; 113 MB of results and only eight steps),
+// 128 x 7168 x 16384 in 20.4 us, 16 x 8 of 256 experts of 2048 x 2048 in 39 us
+// (the weights at 4.6 TB/s). Sharing the steps' instructions between more waves
+// (half the LDS reads) changes nothing: 64 x 64 tiles 21.0 us against 20.7.
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int PATH, int Q>
 __global__ void __launch_bounds__(WM * WN * 64)
 mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
     constexpr int NW = WM * WN;
     constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
     static_assert(FM * 32 * WM == BM && FN * 32 * WN == BN, "whole instructions per wave");
-    // A pair of scales is loaded with the codes of its first step, STAGES steps
-    // ahead, and read last one step after it: so many pairs are there at once.
-    constexpr int PAIRS = STAGES / 2 + 1;
-    constexpr int STAGE = (BM + BN) * 128, SCALES = ScaleStager<BM, BN, NW, PATH>::BYTES;
-    constexpr int RING = STAGES * STAGE + PAIRS * SCALES, OUT = BM * BN * 2;
+    // A group of scales is loaded with the codes of its first step, STAGES steps
+    // ahead, and read last with those of its last: so many groups are there at once.
+    constexpr int GROUPS = (STAGES + Q - 2) / Q + 1;
+    constexpr int STAGE = (BM + BN) * 128, SCALES = ScaleStager<BM, BN, NW, PATH, Q>::BYTES;
+    constexpr int RING = STAGES * STAGE + GROUPS * SCALES, OUT = BM * BN * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > OUT ? RING : OUT];
     uint8_t* const scale_mem = smem + STAGES * STAGE;
     using StA = MxStager<BM, NW>;
     using StB = MxStager<BN, NW>;
-    using StS = ScaleStager<BM, BN, NW, PATH>;
+    using StS = ScaleStager<BM, BN, NW, PATH, Q>;
     // loads a wave has in flight, at least, when only those of the STAGES - 1
     // or STAGES - 2 youngest steps are
     constexpr int L = StA::PER + StB::PER;
-    constexpr int AHEAD1 = (STAGES - 1) * L + (STAGES - 1) / 2 * StS::PER;
-    constexpr int AHEAD2 = (STAGES - 2) * L + (STAGES - 2) / 2 * StS::PER;
+    constexpr int AHEAD1 = (STAGES - 1) * L + (STAGES - 1) / Q * StS::PER;
+    constexpr int AHEAD2 = (STAGES - 2) * L + (STAGES - 2) / Q * StS::PER;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -549,12 +567,12 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
         const uint8_t *scales_a = p.SFA + (int64_t)t.row0 * blocks, *scales_b = p.SFB + rb * blocks;
         ss.init(scales_a, scales_b, last_a, last_b, rows_a * blocks, rows_b * blocks, blocks, wave, lane);
 
-        // a stage: A's codes, B's codes; before those of an even step, its pair of scales
-        auto pair_mem = [&](int step) { return scale_mem + (uint32_t)(step / 2) % PAIRS * SCALES; };
+        // a stage: A's codes, B's codes; before those of a group's first step, its scales
+        auto group_mem = [&](int step) { return scale_mem + (uint32_t)step / Q % GROUPS * SCALES; };
         auto issue = [&](int step, uint8_t* st) {
             const int s = min(step, nsteps - 1);       // past the end: the last one again
             if constexpr (PATH != SHORT)
-                if ((step & 1) == 0) ss.issue(StS::pair_start(s, blocks), pair_mem(step), wave);
+                if (step % Q == 0) ss.issue(StS::group_start(s, blocks), group_mem(step), wave);
             sa.template issue<PATH != WHOLE>((uint32_t)s * STEP, st, wave);
             sb.template issue<PATH != WHOLE>((uint32_t)s * STEP, st + BM * 128, wave);
         };
@@ -562,7 +580,7 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
             if constexpr (PATH == SHORT) ss.fetch(step, blocks, wave, lane);
         };
         auto store = [&](int step) {
-            if constexpr (PATH == SHORT) ss.store(step, blocks, pair_mem(step), wave, lane);
+            if constexpr (PATH == SHORT) ss.store(step, blocks, group_mem(step), wave, lane);
         };
         // Fragment addresses: block 4h + s of row 32 i + l % 32 of the wave's
         // rows; every second fragment's swizzle differs in bit 2 (64 bytes).
@@ -585,8 +603,8 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
         const uint32_t odd_a = (uint32_t)reinterpret_cast<uintptr_t>(scales_a) + (uint32_t)(wm * TM + row) * blocks;
         const uint32_t odd_b = (uint32_t)reinterpret_cast<uintptr_t>(scales_b) + (uint32_t)(wn * TN + row) * blocks;
         auto exps = [&](int step, int (&a)[FM], int (&b)[FN]) {
-            const uint8_t* q = pair_mem(step);
-            const uint32_t ps = StS::pair_start(step, blocks), at = (uint32_t)step * STEP - ps + 4 * h;
+            const uint8_t* q = group_mem(step);
+            const uint32_t ps = StS::group_start(step, blocks), at = (uint32_t)step * STEP - ps + 4 * h;
             StS::read(q, wm * TM + row, at, (odd_a + ps) & 3, a);
             StS::read(q, StS::PAD + wn * TN + row, at, (odd_b + ps) & 3, b);
             if constexpr (PATH == SHIFTED) {
@@ -645,23 +663,22 @@ mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
         if constexpr (FM * FN <= 4) {
             // Small wave tiles: an instruction's worth of products is shorter
             // than an LDS read takes, so a whole step's fragments are read
-            // while the step before is multiplied (64 x 64 tile, 64 rows, N
-            // 4096, K 7168: 10.5 us reading one instruction ahead).
+            // while the step before is multiplied.
             u32x4 fa[2][4][FM], fb[2][4][FN];
             int ea[2][FM], eb[2][FN];
             auto read = [&](int k, const uint8_t* st, auto q) {
-                constexpr int Q = decltype(q)::value;
-                exps(k, ea[Q], eb[Q]);
+                constexpr int B = decltype(q)::value;
+                exps(k, ea[B], eb[B]);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) frags(st, s, fa[Q][s], fb[Q][s]);
+                for (int s = 0; s < 4; ++s) frags(st, s, fa[B][s], fb[B][s]);
             };
             auto last = [&](auto q) {
-                constexpr int Q = decltype(q)::value;
-                static_for<4>([&](auto s) { cut(decltype(s)::value, fa[Q][decltype(s)::value]); });
+                constexpr int B = decltype(q)::value;
+                static_for<4>([&](auto s) { cut(decltype(s)::value, fa[B][decltype(s)::value]); });
             };
             auto multiply = [&](auto q) {
-                constexpr int Q = decltype(q)::value;
-                static_for<4>([&](auto s) { mfma(s, fa[Q][decltype(s)::value], fb[Q][decltype(s)::value], ea[Q], eb[Q]); });
+                constexpr int B = decltype(q)::value;
+                static_for<4>([&](auto s) { mfma(s, fa[B][decltype(s)::value], fb[B][decltype(s)::value], ea[B], eb[B]); });
             };
             constexpr std::integral_constant<int, 0> EVEN{};
             constexpr std::integral_constant<int, 1> ODD{};
@@ -852,9 +869,10 @@ hipError_t launch_skinny(const MxGemmProblem& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// WM x WN waves where K is whole steps, WM2 x WN2 otherwise (more registers:
-// fewer, larger waves keep two workgroups on a compute unit, or avoid spills).
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int WM2 = WM, int WN2 = WN>
+// WM x WN waves and scales Q steps at a time where K is whole steps, WM2 x WN2
+// and pairs otherwise (more registers: fewer, larger waves keep two workgroups
+// on a compute unit, or avoid spills).
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int Q = 2, int WM2 = WM, int WN2 = WN>
 hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
     const uint64_t tiles_n = (p.N + BN - 1) / BN;
     uint64_t tiles_m = (p.M + BM - 1) / BM;
@@ -865,13 +883,13 @@ hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
     }
     if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
     const dim3 grid((uint32_t)(tiles_m * tiles_n));
-    const ScalePath path = scale_path(p.K);
+    const ScalePath path = scale_path<Q>(p.K);
     if (path == WHOLE)
-        mx_tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, WHOLE><<<grid, WM * WN * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+        mx_tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, WHOLE, Q><<<grid, WM * WN * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
     else if (path == SHIFTED)
-        mx_tile_kernel<BM, BN, WM2, WN2, STAGES, GROUPED, SHIFTED><<<grid, WM2 * WN2 * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+        mx_tile_kernel<BM, BN, WM2, WN2, STAGES, GROUPED, SHIFTED, 2><<<grid, WM2 * WN2 * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
     else
-        mx_tile_kernel<BM, BN, WM2, WN2, STAGES, GROUPED, SHORT><<<grid, WM2 * WN2 * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
+        mx_tile_kernel<BM, BN, WM2, WN2, STAGES, GROUPED, SHORT, 2><<<grid, WM2 * WN2 * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
     return hipGetLastError();
 }
 
@@ -908,9 +926,9 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
         // us with 32 x 128, 64 x 128 and 128 x 128 tiles: 4 rows 51, 52, 55;
         // 16 rows 59, 59, 65; 32 rows 72, 67, 73; 141 rows 161, 126, 118.
         const uint64_t mean = p.M / p.E;
-        if (mean < 16) return launch_tile<32, 128, 1, 4, 2, true>(p, stream);
+        if (mean < 16) return launch_tile<32, 128, 1, 4, 2, true, 4>(p, stream);
         if (mean < 64) return launch_tile<64, 128, 2, 2, 3, true>(p, stream);
-        return launch_tile<128, 128, 4, 2, 2, true, 2, 2>(p, stream);
+        return launch_tile<128, 128, 4, 2, 2, true, 4, 2, 2>(p, stream);
     }
     // Up to 16 rows, where 64-column tiles would fill under a third of the
     // compute units: 1 x 4096 x 7168 5.0 us against 8.0 us with the smallest
@@ -925,12 +943,12 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
         int bm, bn;
         double fixed, alone, paired;   // paired 0: one workgroup fills a compute unit's LDS
     };
-    static constexpr Tile tiles[] = {{256, 256, 4.0, 2.15, 0},    {256, 128, 2.1, 1.14, 0},   {128, 128, 2.0, 0.61, 1.3},
-                                     {128, 64, 2.5, 0.45, 0.77}, {64, 64, 1.5, 0.31, 0.54}, {32, 64, 1.5, 0.23, 0.4}};
+    static constexpr Tile tiles[] = {{256, 256, 3.5, 2.15, 0},   {256, 128, 3.2, 1.13, 0},   {128, 128, 2.0, 0.61, 1.22},
+                                     {64, 64, 1.5, 0.28, 0.47}, {32, 64, 1.5, 0.23, 0.4}};
     const double steps = (p.K + 255) / 256;
     int best = 0;
     double least = 0;
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 5; ++i) {
         const Tile& c = tiles[i];
         const uint64_t n = (uint64_t)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn), cu = p.cus;
         double t;
@@ -944,15 +962,14 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
         if (i == 0 || t < least) best = i, least = t;
     }
     switch (best) {
-        case 0: return launch_tile<256, 256, 2, 4, 2, false, 2, 2>(p, stream);
+        case 0: return launch_tile<256, 256, 2, 4, 2, false, 2, 2, 2>(p, stream);
         case 1: return launch_tile<256, 128, 4, 2, 3, false>(p, stream);
         case 2:
             // one to a compute unit: LDS for four stages (512 x 7168 x 16384: 41 us, 50 with two)
             if ((uint64_t)((p.M + 127) / 128) * ((p.N + 127) / 128) <= (uint64_t)p.cus)
-                return launch_tile<128, 128, 4, 2, 4, false, 2, 2>(p, stream);
-            return launch_tile<128, 128, 4, 2, 2, false, 2, 2>(p, stream);
-        case 3: return launch_tile<128, 64, 2, 2, 3, false>(p, stream);
-        case 4: return launch_tile<64, 64, 2, 2, 4, false>(p, stream);
+                return launch_tile<128, 128, 4, 2, 4, false, 2, 2, 2>(p, stream);
+            return launch_tile<128, 128, 4, 2, 2, false, 4, 2, 2>(p, stream);
+        case 3: return launch_tile<64, 64, 2, 2, 4, false, 4>(p, stream);
     }
     return launch_tile<32, 64, 1, 2, 4, false>(p, stream);
 }

@@ -47,7 +47,7 @@ def test_product_at_full_size(m, n, k):
 # other length; few rows with K that ends inside a turn of the eight waves.
 TILES = [(9, 500, 4128), (16, 60, 8192), (100, 4100, 32), (100, 4099, 480), (2812, 1430, 288), (100, 9000, 4096), (100, 9000, 4128),
          (129, 12000, 512), (129, 12001, 544), (129, 12002, 160), (2000, 4100, 512), (2001, 4100, 480), (300, 12000, 1056),
-         (300, 12004, 352), (3000, 4100, 2080), (3001, 4097, 416)]
+         (300, 12004, 352), (3000, 4100, 2080), (3001, 4097, 416), (1000, 4100, 4096), (1001, 4099, 4128), (2000, 4104, 1280), (130, 12000, 1792), (5000, 3000, 1024)]
 
 
 @pytest.mark.parametrize("m,n,k", TILES)
