@@ -500,12 +500,13 @@ struct ScaleStager {
 // The matrix instruction takes B first, so a lane ends up with four
 // consecutive columns of one row of C.
 //
-// Bound by staging, about 50 bytes per ns and compute unit from L2 to LDS with
-// every tile shape, and by power: 4096 x 4096 x 8192 in 76 us (3.6 PFLOP/s),
-// 5120 x 11008 x 2048 in 85 us (2.7; 113 MB of results and only eight steps),
-// 128 x 7168 x 16384 in 20.4 us, 16 x 8 of 256 experts of 2048 x 2048 in 39 us
-// (the weights at 4.6 TB/s). Sharing the steps' instructions between more waves
-// (half the LDS reads) changes nothing: 64 x 64 tiles 21.0 us against 20.7.
+// Bound by the cache lines a step's loads touch (fewer scale lines made every
+// tile faster, more stages or fewer LDS reads did not: with each wave taking
+// one of a step's instructions for the whole tile 64 x 64 took 21.0 us against
+// 20.7) and, at 3 PFLOP/s and more, by power: 4096 x 4096 x 8192 in 72.5 us (3.8
+// PFLOP/s), 5120 x 11008 x 2048 in 83 us (2.8; 113 MB of results and only eight
+// steps), 128 x 7168 x 16384 in 19.2 us, 16 x 8 of 256 experts of 2048 x 2048 in
+// 39.7 us (the weights at 4.8 TB/s).
 template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int PATH, int Q>
 __global__ void __launch_bounds__(WM * WN * 64)
 mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
