@@ -42,6 +42,9 @@ namespace {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+// the same at any element: global memory takes unaligned accesses
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float NEG_INF = -__builtin_inff();
@@ -98,8 +101,31 @@ __device__ __forceinline__ double larger(double a, double b) {
     return r;
 }
 
+// The words of a load that starts `past` elements early, moved down by as many;
+// -infinity behind them. BF16: two elements a word.
+template <bool F32, int W>
+__device__ __forceinline__ void move_down(uint32_t (&w)[W], int past) {
+    constexpr uint32_t FILL = F32 ? 0xFF800000u : 0xFF80FF80u;
+    constexpr int PER = F32 ? 1 : 2;
+    auto by = [&](int words, bool is) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = is ? (i + words < W ? w[i + words] : FILL) : w[i];
+    };
+    by(W, past >= W * PER);
+    if constexpr (W == 4) by(2, past & (2 * PER));
+    by(1, past & PER);
+    if constexpr (!F32) {
+        const uint32_t half = past & 1 ? 2 : 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = __builtin_amdgcn_alignbyte(i + 1 < W ? w[i + 1] : FILL, w[i], half);
+    }
+}
+
 // A lane's VPL logits of row t; -infinity past E. VEC: rows start on whole
-// loads and E is a multiple of a load's elements.
+// loads and E is a multiple of a load's elements. Otherwise loads start at any
+// element, and one that would end past the row starts earlier, so that it ends
+// with it (24670 x 470, BF16, k = 3, with its gradient: a call 114 us element
+// by element; now the kernels' 17.7, 26.9 and 18.8 us).
 template <bool F32, int VPL, bool VEC>
 __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int e0, float (&v)[VPL]) {
     if constexpr (VEC && F32) {
@@ -126,18 +152,45 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
             }
         }
     } else {
-        // every lane loads (past E, the row's last logit again): a branch
-        // around each load would wait for one after the other
+        constexpr int W = F32 || VPL % 8 == 0 ? 4 : 2, N = F32 ? W : 2 * W;      // words and elements a load
+        if (E >= N) {
+            uint32_t w[VPL / N][W];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int64_t at = t * E + min(e0 + i, E - 1);
-            if constexpr (F32)
-                v[i] = static_cast<const float*>(logits)[at];
-            else
-                v[i] = __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
+            for (int i = 0; i < VPL / N; ++i) {
+                const int64_t at = t * E + min(e0 + i * N, E - N);
+                const void* q = F32 ? (const void*)(static_cast<const float*>(logits) + at)
+                                    : (const void*)(static_cast<const uint16_t*>(logits) + at);
+                if constexpr (W == 4) {
+                    const u32x4 x = *static_cast<const u32x4_any*>(q);
+                    w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                } else {
+                    const u32x2 x = *static_cast<const u32x2_any*>(q);
+                    w[i][0] = x.x, w[i][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VPL / N; ++i) {
+                move_down<F32>(w[i], max(e0 + (i + 1) * N - E, 0));
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    v[i * N + j] = __builtin_bit_cast(float, F32       ? w[i][j % W]
+                                                             : j % 2 == 0 ? w[i][j / 2 % W] << 16
+                                                                          : w[i][j / 2 % W] & 0xFFFF0000u);
+            }
+        } else {
+            // every lane loads (past E, the row's last logit again): a branch
+            // around each load would wait for one after the other
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int64_t at = t * E + min(e0 + i, E - 1);
+                if constexpr (F32)
+                    v[i] = static_cast<const float*>(logits)[at];
+                else
+                    v[i] = __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? v[i] : NEG_INF;
         }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? v[i] : NEG_INF;
     }
 }
 
@@ -663,13 +716,32 @@ route_backward_kernel(RouteBackwardProblem p) {
                 if (e0 + i < E) *reinterpret_cast<Store*>(o + i) = x;
             }
         } else {
+// whole pieces at any element, and what is left of the last one by itself
+            constexpr int W = F32 || VPL % 8 == 0 ? 4 : 2, N = F32 ? W : 2 * W;
+            const int64_t at = t * E + e0;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (e0 + i >= E) continue;
-                if constexpr (F32)
-                    static_cast<float*>(p.dlogits)[t * E + e0 + i] = v[i];
-                else
-                    static_cast<__bf16*>(p.dlogits)[t * E + e0 + i] = (__bf16)v[i];
+            for (int i = 0; i < VPL; i += N) {
+                uint32_t w[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    w[j] = F32 ? __builtin_bit_cast(uint32_t, v[i + j]) : pack_bf16x2(v[i + 2 * j % N], v[i + (2 * j + 1) % N]);
+                if (e0 + i + N <= E) {
+                    void* q = F32 ? (void*)(static_cast<float*>(p.dlogits) + at + i)
+                                  : (void*)(static_cast<uint16_t*>(p.dlogits) + at + i);
+                    if constexpr (W == 4)
+                        *static_cast<u32x4_any*>(q) = u32x4{w[0], w[1], w[2], w[3]};
+                    else
+                        *static_cast<u32x2_any*>(q) = u32x2{w[0], w[1]};
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        if (e0 + i + j >= E) continue;
+                        if constexpr (F32)
+                            static_cast<float*>(p.dlogits)[at + i + j] = v[i + j];
+                        else
+                            static_cast<__bf16*>(p.dlogits)[at + i + j] = (__bf16)v[i + j];
+                    }
+                }
             }
         }
     }
