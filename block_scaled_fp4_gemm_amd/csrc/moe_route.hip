@@ -125,7 +125,7 @@ __device__ __forceinline__ void move_down(uint32_t (&w)[W], int past) {
 // loads and E is a multiple of a load's elements. Otherwise loads start at any
 // element, and one that would end past the row starts earlier, so that it ends
 // with it (24670 x 470, BF16, k = 3, with its gradient: a call 114 us element
-// by element; now the kernels' 17.7, 26.9 and 18.8 us).
+// by element; now the kernels' 17.7, 15.8 and 18.8 us).
 template <bool F32, int VPL, bool VEC>
 __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int e0, float (&v)[VPL]) {
     if constexpr (VEC && F32) {
@@ -580,7 +580,7 @@ route_place_kernel(RouteProblem p, int rows_per_block, int blocks) {
     const int tid = threadIdx.x, E = (int)p.E, b = (int)blockIdx.x - 1;
     const RouteWs ws = split_ws(p.ws, (uint64_t)blocks, p.E);
     // Sums over the workgroups of the first kernel. A thread takes four experts
-    // (one, where rows are not whole 16-byte loads) and every `segs`-th
+    // (two or one, where rows are not whole loads of four) and every `segs`-th
     // workgroup, with its loads in flight at once; the partial sums meet in
     // LDS and are added in order.
     if (tid == 0) live = 0;
@@ -590,6 +590,8 @@ route_place_kernel(RouteProblem p, int rows_per_block, int blocks) {
     int n = b < 0 && tid < blocks ? ws.live[tid] : 0;
     if (E % 4 == 0)
         sum_blocks<4>(ws, E, blocks, b, cnt, off, before, mean, tid);
+    else if (E % 2 == 0)
+        sum_blocks<2>(ws, E, blocks, b, cnt, off, before, mean, tid);
     else
         sum_blocks<1>(ws, E, blocks, b, cnt, off, before, mean, tid);
     if (b < 0) {

@@ -53,7 +53,7 @@ def _check(x, k, got, valid=None, normalize=True, what=""):
 
 SIZES = [(1, 1, 1), (1, 4, 2), (3, 5, 5), (16, 256, 8), (17, 256, 8), (31, 64, 6), (32, 128, 4), (33, 8, 2), (50, 65, 3), (100, 160, 6), (257, 16, 16),
          (300, 257, 7), (70, 512, 8), (40, 513, 10), (1000, 256, 8), (90, 1000, 16), (64, 1024, 16), (2255, 60, 1), (20000, 24, 4),
-         (64, 300, 5), (65, 33, 4), (16385, 100, 3), (17000, 256, 8), (600, 1024, 9)]
+         (64, 300, 5), (65, 33, 4), (16385, 100, 3), (17000, 256, 8), (600, 1024, 9), (700, 470, 3), (100, 6, 2), (3000, 1022, 9), (90, 2, 1)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
