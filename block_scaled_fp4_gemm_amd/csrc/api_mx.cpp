@@ -3,6 +3,7 @@
 // plain host code and nothing is enqueued unless every check passes.
 #include "api_checks.hpp"
 #include "bg_internal.hpp"
+#include "mx_tiles.hpp"
 
 namespace {
 
@@ -92,6 +93,7 @@ bg_status gemm_mxfp4(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, con
     if (!dims_ok(M, N, K) || K % 32 != 0 || K > kMaxMxK || !fits(M, K, 1, 1) || !fits(N, K, 1, 1) || !fits(M, N, 1, 2))
         return BG_ERR_SHAPE;
     if (M == 0 || N == 0) return BG_OK;
+    if (!mx_dense_launches(M, N, K)) return BG_ERR_SHAPE;
     bg_status s = check_mx_gemm(A, SFA, B, SFB, nullptr, C, M, N, K, 1);
     if (s != BG_OK) return s;
     uint32_t cus = 0;
@@ -107,6 +109,7 @@ bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t
         !fits(S, N, 1, 2))
         return BG_ERR_SHAPE;
     if (S == 0 || N == 0 || E == 0) return BG_OK;
+    if (mx_grouped_tile(S, N, K, E) < 0) return BG_ERR_SHAPE;
     if (offsets == nullptr) return BG_ERR_NULL;
     bg_status s = check_mx_gemm(A, SFA, B, SFB, offsets, C, S, N, K, E);
     if (s != BG_OK) return s;

@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "bg_internal.hpp"
+#include "mx_tiles.hpp"
 #include "tile_order.hpp"
 
 #pragma clang fp contract(off)
@@ -239,9 +240,6 @@ __device__ __forceinline__ TileRows group_tile(const int32_t* offsets, int E, in
 
 // Workgroups of a kernel that loops over the rest (a launch holds fewer than 2^32 threads).
 uint32_t grid_of(uint64_t groups) { return (uint32_t)(groups < (1u << 20) ? groups : (1u << 20)); }
-
-// A grid of one workgroup of at most 1024 threads per tile.
-bool tiles_fit(uint64_t tiles) { return tiles < (1u << 22); }
 
 // Compile-time loops over a constant's values.
 template <int N, class F>
@@ -870,20 +868,17 @@ hipError_t launch_skinny(const MxGemmProblem& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// WM x WN waves and scales Q steps at a time where K is whole steps, WM2 x WN2
-// and pairs otherwise (more registers: fewer, larger waves keep two workgroups
-// on a compute unit, or avoid spills).
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int Q = 2, int WM2 = WM, int WN2 = WN>
+// Tile I of its table. WM x WN waves and scales Q steps at a time where K is
+// whole steps, WM2 x WN2 and pairs otherwise (more registers: fewer, larger
+// waves keep two workgroups on a compute unit, or avoid spills).
+template <int I, bool GROUPED, int WM, int WN, int STAGES, int Q = 2, int WM2 = WM, int WN2 = WN>
 hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
-    const uint64_t tiles_n = (p.N + BN - 1) / BN;
-    uint64_t tiles_m = (p.M + BM - 1) / BM;
-    if (GROUPED) {
-        // every expert may end in a partly filled tile; eight stretches of at
-        // least as many tiles as exist
-        tiles_m = (p.M / BM + (p.E < p.M ? p.E : p.M) + 7) / 8 * 8;
-    }
-    if (!tiles_fit(tiles_m * tiles_n)) return hipErrorInvalidValue;
-    const dim3 grid((uint32_t)(tiles_m * tiles_n));
+    constexpr MxTile T = GROUPED ? kMxGrouped[I] : kMxDense[I];
+    constexpr int BM = T.bm, BN = T.bn;
+    static_assert(T.whole == WM * WN * 64 && T.other == WM2 * WN2 * 64, "threads of the grid's limit");
+    const uint32_t tiles_n = (uint32_t)mx_ceil(p.N, BN);
+    const uint32_t tiles_m = (uint32_t)(GROUPED ? mx_tiles_m_grouped(T, p.M, p.E) : mx_tiles_m(T, p.M));
+    const dim3 grid(tiles_m * tiles_n);
     const ScalePath path = scale_path<Q>(p.K);
     if (path == WHOLE)
         mx_tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, WHOLE, Q><<<grid, WM * WN * 64, 0, stream>>>(p, (int)tiles_m, (int)tiles_n);
@@ -923,56 +918,30 @@ hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
 
 hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
     if (p.offsets != nullptr) {
-        // By the rows an expert has on average. 256 experts, N 1024, K 2048,
-        // us with 32 x 128, 64 x 128 and 128 x 128 tiles: 4 rows 51, 52, 55;
-        // 16 rows 59, 59, 65; 32 rows 72, 67, 73; 141 rows 161, 126, 118.
-        const uint64_t mean = p.M / p.E;
-        if (mean < 16) return launch_tile<32, 128, 1, 4, 2, true, 4>(p, stream);
-        if (mean < 64) return launch_tile<64, 128, 2, 2, 3, true>(p, stream);
-        return launch_tile<128, 128, 4, 2, 2, true, 4, 2, 2>(p, stream);
+        switch (mx_grouped_tile(p.M, p.N, p.K, p.E)) {
+            case MX_G32x128: return launch_tile<MX_G32x128, true, 1, 4, 2, 4>(p, stream);
+            case MX_G64x128: return launch_tile<MX_G64x128, true, 2, 2, 3>(p, stream);
+            case MX_G128x128: return launch_tile<MX_G128x128, true, 4, 2, 2, 4, 2, 2>(p, stream);
+        }
+        return hipErrorInvalidValue;
     }
     // Up to 16 rows, where 64-column tiles would fill under a third of the
     // compute units: 1 x 4096 x 7168 5.0 us against 8.0 us with the smallest
     // tile, 16 x 4096 x 7168 6.3 / 8.1 us (16 x 7168 x 16384: 20 / 15 us).
     if (p.M <= 16 && (uint64_t)p.N * 3 <= (uint64_t)p.cus * 64)
         return p.K >= 8 * 512 ? launch_skinny<8>(p, stream) : launch_skinny<4>(p, stream);
-    // Otherwise the tile whose time, counted in rounds over the compute units,
-    // is least: us per tile and per step of 256 K elements, alone on a compute
-    // unit and as one of two (fitted to 20 shapes from 32 x 4096 x 7168 to
-    // 4096 x 4096 x 8192, most within 10%).
-    struct Tile {
-        int bm, bn;
-        double fixed, alone, paired;   // paired 0: one workgroup fills a compute unit's LDS
-    };
-    static constexpr Tile tiles[] = {{256, 256, 3.5, 2.15, 0},   {256, 128, 3.2, 1.13, 0},   {128, 128, 2.0, 0.61, 1.22},
-                                     {64, 64, 1.5, 0.28, 0.47}, {32, 64, 1.5, 0.23, 0.4}};
-    const double steps = (p.K + 255) / 256;
-    int best = 0;
-    double least = 0;
-    for (int i = 0; i < 5; ++i) {
-        const Tile& c = tiles[i];
-        const uint64_t n = (uint64_t)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn), cu = p.cus;
-        double t;
-        if (c.paired == 0) {
-            t = (double)((n + cu - 1) / cu) * (c.fixed + steps * c.alone);
-        } else {
-            const uint64_t rest = n % (2 * cu);
-            t = (double)(n / (2 * cu)) * (c.fixed + steps * c.paired);
-            if (rest != 0) t += c.fixed + steps * (rest <= cu ? c.alone : c.paired);
-        }
-        if (i == 0 || t < least) best = i, least = t;
-    }
-    switch (best) {
-        case 0: return launch_tile<256, 256, 2, 4, 2, false, 2, 2, 2>(p, stream);
-        case 1: return launch_tile<256, 128, 4, 2, 3, false>(p, stream);
-        case 2:
+    switch (mx_dense_tile(p.M, p.N, p.K, p.cus)) {
+        case MX_256x256: return launch_tile<MX_256x256, false, 2, 4, 2, 2, 2, 2>(p, stream);
+        case MX_256x128: return launch_tile<MX_256x128, false, 4, 2, 3>(p, stream);
+        case MX_128x128:
             // one to a compute unit: LDS for four stages (512 x 7168 x 16384: 41 us, 50 with two)
-            if ((uint64_t)((p.M + 127) / 128) * ((p.N + 127) / 128) <= (uint64_t)p.cus)
-                return launch_tile<128, 128, 4, 2, 4, false, 2, 2, 2>(p, stream);
-            return launch_tile<128, 128, 4, 2, 2, false, 4, 2, 2>(p, stream);
-        case 3: return launch_tile<64, 64, 2, 2, 4, false, 4>(p, stream);
+            if (mx_ceil(p.M, 128) * mx_ceil(p.N, 128) <= p.cus)
+                return launch_tile<MX_128x128, false, 4, 2, 4, 2, 2, 2>(p, stream);
+            return launch_tile<MX_128x128, false, 4, 2, 2, 4, 2, 2>(p, stream);
+        case MX_64x64: return launch_tile<MX_64x64, false, 2, 2, 4, 4>(p, stream);
+        case MX_32x64: return launch_tile<MX_32x64, false, 1, 2, 4>(p, stream);
     }
-    return launch_tile<32, 64, 1, 2, 4, false>(p, stream);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace bg

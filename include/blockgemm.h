@@ -445,7 +445,9 @@ bg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, void* ou
  * codes and the E8M0 scales as they are stored. The summation order is
  * unspecified but fixed by the shape: repeated calls return identical bits.
  *
- *  K % 32 == 0 and K <= 2^24 (BG_ERR_SHAPE otherwise).
+ *  K % 32 == 0 and K <= 2^24 (BG_ERR_SHAPE otherwise). A launch's grid holds
+ *     every product with ceil(M / 256) * ceil(N / 256) < 2^23; BG_ERR_SHAPE
+ *     past that where no tile's grid holds it.
  *  A: [M, K/2], SFA: [M, K/32], B: [N, K/2], SFB: [N, K/32] bytes, read. Scales
  *     are read in aligned four-byte words: where an array of them ends inside
  *     a word, the up to three bytes behind it in that word are read too (never
@@ -469,8 +471,10 @@ bg_status gemm_mxfp4(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, con
  *           unspecified). 4-byte aligned.
  *  C: [S, N] BF16. Rows before offsets[0] and from offsets[E] on are left as
  *     they were. C must not overlap an input (BG_ERR_ALIAS).
- *  K % 32 == 0, K <= 2^24 and E <= 1024 (BG_ERR_SHAPE otherwise). E == 0, S == 0
- *  or N == 0: nothing to do.
+ *  K % 32 == 0, K <= 2^24 and E <= 1024 (BG_ERR_SHAPE otherwise). A launch's
+ *  grid holds every product with (S / 128 + min(E, S) + 7) * ceil(N / 128) <
+ *  2^23; BG_ERR_SHAPE past that where no tile's grid holds it. E == 0, S == 0 or
+ *  N == 0: nothing to do.
  */
 bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB,
                              const int32_t* offsets, uint16_t* C, uint32_t S, uint32_t N, uint32_t K, uint32_t E,
