@@ -57,6 +57,7 @@ bg_status mxfp4_quantize(const void* x, int x_type, uint32_t ldx, const int32_t*
     if (!dims_ok(M, R, K) || ldx > kMaxDim || K % 32 != 0 || ldx < K || !type_ok(x_type)) return BG_ERR_SHAPE;
     if (rows == nullptr && R != M) return BG_ERR_SHAPE;
     if (!fits(M, ldx, 1, type_size(x_type)) || !fits(R, K, 1, 1)) return BG_ERR_SHAPE;
+    if ((uint64_t)R * mx_quant_pieces(K) > 0xFFFFFFFFu) return BG_ERR_SHAPE;
     if (R == 0 || K == 0) return BG_OK;
     const uint64_t x_bytes = M == 0 ? 0 : ((uint64_t)(M - 1) * ldx + K) * type_size(x_type);
     const uint64_t c_bytes = (uint64_t)R * (K / 2), s_bytes = (uint64_t)R * (K / 32);

@@ -892,9 +892,8 @@ hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_mxfp4_quantize(const MxQuantProblem& p, hipStream_t stream) {
-    const uint32_t segs = (p.K + 511) / 512;
-    const uint64_t waves = (uint64_t)p.R * segs;
-    if (waves > 0xFFFFFFFFu) return hipErrorInvalidValue;      // 1 TB of codes, or rows of one wave: R itself
+    const uint32_t segs = mx_quant_pieces(p.K);
+    const uint64_t waves = (uint64_t)p.R * segs;               // < 2^32: checked
     const uint32_t per_seg = segs == 1 ? 0xFFFFFFFFu : (uint32_t)(((uint64_t)1 << 32) / segs) + ((((uint64_t)1 << 32) % segs) != 0);
     const dim3 grid(grid_of((waves + 7) / 8));
     const bool f32 = p.type == BG_F32;

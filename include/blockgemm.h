@@ -424,6 +424,7 @@ typedef enum bg_type { BG_BF16 = 0, BG_F32 = 1 } bg_type;
  *          aligned.
  *  codes:  [R, K/2] bytes, scales: [R, K/32] bytes, written; must not overlap
  *          x, rows or each other (BG_ERR_ALIAS).
+ *  R * ceil(K / 512) < 2^32 (BG_ERR_SHAPE otherwise).
  */
 bg_status mxfp4_quantize(const void* x, int x_type, uint32_t ldx, const int32_t* rows, uint8_t* codes,
                          uint8_t* scales, uint32_t M, uint32_t R, uint32_t K, void* stream);

@@ -36,3 +36,10 @@ def test_sizes_within_the_limits_pass_the_checks():
         assert L.gemm_mxfp4(A, SA, B, SB, C, m, n, k, None) == bg.BG_ERR_DEVICE, (m, n, k)
     for s, n, k, e in [((1 << 29) + 5, 3, 32, 2), (1 << 24, 4096, 2048, 256), ((1 << 30) - (1 << 18), 1, 1024, 1024)]:
         assert L.gemm_mxfp4_grouped(A, SA, B, SB, O, C, s, n, k, e, None) == bg.BG_ERR_DEVICE, (s, n, k, e)
+    assert L.mxfp4_quantize(A, BF16, 544, None, B, SB, BIG, BIG, 544, None) == bg.BG_ERR_DEVICE
+
+
+def test_quantisation_of_more_pieces_than_it_numbers_is_refused_as_a_shape():
+    q = L.mxfp4_quantize
+    assert q(A, BF16, 1056, None, B, SB, BIG, BIG, 1056, None) == bg.BG_ERR_SHAPE
+    assert q(A, F32, 1 << 20, O, B, SB, 4, 1 << 21, 1 << 20, None) == bg.BG_ERR_SHAPE
