@@ -106,14 +106,22 @@ constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 
 constexpr uint32_t kMaxExperts = 1024;   // routing and grouped products
 constexpr uint32_t kMaxTopK = 16;
 
-// Up to this many rows one workgroup routes alone, in one launch, without a workspace.
+// Up to this many rows one workgroup routes alone, in one launch, without a
+// workspace. 256 experts, k = 8, us alone and in two launches, BF16: 32 rows 7.8
+// and 11.5, 64 rows 9.8 and 11.6, 96 rows 13.0 and 11.7; FP32: 9.2 and 12.7, 12.8
+// and 12.9, 17.0 and 13.0.
 constexpr uint32_t kRouteOneBlock = 64;
 // Above this many rows the workgroups of moe_route have 1024 threads, else 512.
+// 256 experts, k = 8, us of a call with 512 and 1024, BF16: 2048 rows 13.6 and
+// 14.8, 4510 rows 16.1 and 16.3, 16384 rows 21.8 and 21.3, 65536 rows 38.9 and
+// 36.4; FP32: 15.1 and 17.2, 18.0 and 19.0, 25.8 and 24.7, 50.0 and 45.1. (From
+// 8192 rows on 1024 is level or ahead: 19.4 and 16.9 there, 18.3 and 18.0 at 12288.)
 constexpr uint32_t kRouteWide = 16384;
-// Rows per workgroup of moe_route: 256 workgroups at most, so that each can sum
-// the counts of all the others by itself, of whole passes (32 tokens per 512
-// threads where 16 lanes hold one), but fewer than 2^16 rows, so that counts
-// fit 16 bits.
+// Rows per workgroup of moe_route: of whole passes (32 tokens per 512 threads
+// where 16 lanes hold one), as many as leave at most 256 workgroups, so that each
+// can sum the counts of all the others by itself; but fewer than 2^16 rows, so
+// that counts fit 16 bits. Past 256 * 65472 rows there are more workgroups, and
+// that sum grows as the square of the rows.
 constexpr uint32_t kRouteMaxRows = 65472;
 inline uint32_t route_rows_per_block(uint32_t T) {
     const uint32_t pass = T > kRouteWide ? 64 : 32;

@@ -19,17 +19,19 @@
 //    by the first method: 65536 x 256 in 45 us.)
 //
 // The dispatch order is that of (expert, row). Workgroups own consecutive
-// rows, at most 256 of them; the first kernel counts per workgroup and expert,
-// the second sums the counts of the workgroups before its own, ranks the
-// choices among its rows and writes the places; one more workgroup of it adds
-// the statistics. All sums over rows are added in a fixed order.
+// rows, at most 256 of them up to 16.7 million rows and one per 65472 beyond;
+// the first kernel counts per workgroup and expert, the second sums the counts
+// of the workgroups before its own (each of them reads all: the square of their
+// number), ranks the choices among its rows and writes the places; one more
+// workgroup of it adds the statistics. All sums over rows are added in a fixed
+// order.
 //
-// Measured, 256 experts, k = 8, BF16 logits, 65536 / 4510 rows: the first
-// kernel 22.9 / 6.8 us (bound by the choices' vector operations: 1.5 TB/s), the
-// second 15.3 / 10.1 (latencies: the sums, then places scattered over 2 MB),
-// the gradient 19.1 / 7.7 (3.5 TB/s of logits, gradients and choices). With
-// FP32 logits the first takes 33.4 and the gradient 33.7 (4 TB/s). One launch
-// does 16 rows in 8.6.
+// Traced, 256 experts, k = 8, BF16 logits, 65536 / 4510 rows: the first kernel
+// 22.6 / 6.6 us (about 16 of the 22.6 are the choices' vector operations, the
+// rest the loads at the top of each pass: 1.5 TB/s), the second 15.6 / 10.0
+// (latencies: the sums, then places scattered over 2 MB), the gradient 19.4 /
+// 7.4 (3.5 TB/s of logits, gradients and choices). With FP32 logits the first
+// takes 31.2 and the gradient 33.1 (4 TB/s). One launch does 16 rows in 8.4.
 #include <type_traits>
 
 #include "bg_internal.hpp"
@@ -718,7 +720,7 @@ route_backward_kernel(RouteBackwardProblem p) {
                 if (e0 + i < E) *reinterpret_cast<Store*>(o + i) = x;
             }
         } else {
-// whole pieces at any element, and what is left of the last one by itself
+            // whole pieces at any element, and what is left of the last one by itself
             constexpr int W = F32 || VPL % 8 == 0 ? 4 : 2, N = F32 ? W : 2 * W;
             const int64_t at = t * E + e0;
 #pragma unroll

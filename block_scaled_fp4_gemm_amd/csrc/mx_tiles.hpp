@@ -74,10 +74,11 @@ inline int mx_dense_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
     return best;
 }
 
-// By the rows an expert has on average. 256 experts, N 1024, K 2048, us with
-// 32 x 128, 64 x 128 and 128 x 128 tiles: 4 rows 51, 52, 55; 16 rows 59, 59, 65;
-// 32 rows 72, 67, 73; 141 rows 161, 126, 118. A larger tile where a launch does
-// not hold that one's grid; -1 where none does.
+// By the rows an expert has on average. 256 experts of unequal load, N 1024, K
+// 2048, us with 32 x 128, 64 x 128 and 128 x 128 tiles: 4 rows 54, 54, 60; 16 rows
+// 59, 61, 68; 32 rows 68, 67, 72; 64 rows 95, 81, 80; 141 rows 158, 127, 107. N
+// 2048: 4 rows 105, 106, 120; 32 rows 133, 130, 140; 64 rows 179, 156, 151. A
+// larger tile where a launch does not hold that one's grid; -1 where none does.
 inline int mx_grouped_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
     const uint64_t mean = M / E;
     int i = mean < 16 ? MX_G32x128 : mean < 64 ? MX_G64x128 : MX_G128x128;

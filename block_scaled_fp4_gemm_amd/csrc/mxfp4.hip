@@ -43,11 +43,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // scale and rounds (nearest, ties to even, saturating at 6), straight from
 // BF16 pairs or FP32.
 //
-// Bound by memory: 5120 x 11008 BF16 in 22.8 us (6.3 TB/s; reading back 21.8),
-// 36080 rows of 2048 gathered from 4510 in 28.3 us. With values unpacked and
-// scaled one by one, a 64-bit division per wave and one piece per wave the
-// vector units were the limit: 28.9 and 35.5 us; one piece per wave alone 25.0
-// and 30.7.
+// Bound by memory: 5120 x 11008 in 28.1 us from BF16 and 49.5 us from FP32 over
+// three inputs in turn (5.1 and 5.2 TB/s; a copy reaches 4.8), 22.8 us with the
+// BF16 input still in the last-level cache. 36080 rows of 2048 gathered from
+// 4510 take 28.3 us: a token is read, converted and written once per listing.
+// With values unpacked and scaled one by one, a 64-bit division per wave and one
+// piece per wave the vector units were the limit: 28.9 us (cached input) and
+// 35.5 us (gathered); one piece per wave alone 25.0 and 30.7.
 // ---------------------------------------------------------------------------
 
 // Eight elements as loaded: FP32 in eight words, BF16 in pairs in four.
@@ -157,7 +159,7 @@ mxfp4_quantize_kernel(MxQuantProblem p, uint32_t segs, uint32_t per_seg, uint32_
 
 // ---------------------------------------------------------------------------
 // Reading back: four code bytes, eight values, per lane and step; 5120 x 11008
-// to BF16 in 21.8 us (6.6 TB/s).
+// to BF16 in 21.8 us (6.5 TB/s), to FP32 in 44.6 us (5.7 TB/s): the writes.
 // ---------------------------------------------------------------------------
 
 // 2^(s - 127) as FP32 (s = 0: the subnormal 2^-127; s = 255: NaN).
@@ -358,9 +360,9 @@ constexpr ScalePath scale_path(uint32_t K) {
 
 // Scales of the BM rows of A and the BN rows of B of a tile, a group of Q steps
 // (two or four) at a time as [row][GROUP] bytes in LDS, by direct loads of 16
-// bytes a lane. What a load costs is the cache lines it touches: a step's 8
-// bytes of scales are one, as many as its 128 bytes of codes, so groups cut
-// the lines a row and step touches from 2 to 1.5 (pairs) or 1.25 (fours):
+// bytes a lane. A step's 8 bytes of scales touch a cache line, as many as its
+// 128 bytes of codes; groups cut the lines a row and step touches from 2 to 1.5
+// (pairs) or 1.25 (fours), and that made every tile faster that kept its stages:
 // 64 x 64 tiles, 128 x 7168 x 16384, 27 us step by step, 20.8 in pairs, 19.2 in
 // fours; 128 x 128 tiles, 4096 x 4096 x 8192, 88.8 us in pairs and 82.4 in
 // fours; the experts' tiles of 32 x 128, 16 x 8 of 256 of 2048 x 2048, 41.0 and
@@ -498,13 +500,20 @@ struct ScaleStager {
 // The matrix instruction takes B first, so a lane ends up with four
 // consecutive columns of one row of C.
 //
-// Bound by the cache lines a step's loads touch (fewer scale lines made every
-// tile faster, more stages or fewer LDS reads did not: with each wave taking
-// one of a step's instructions for the whole tile 64 x 64 took 21.0 us against
-// 20.7) and, at 3 PFLOP/s and more, by power: 4096 x 4096 x 8192 in 72.5 us (3.8
-// PFLOP/s), 5120 x 11008 x 2048 in 83 us (2.8; 113 MB of results and only eight
-// steps), 128 x 7168 x 16384 in 19.2 us, 16 x 8 of 256 experts of 2048 x 2048 in
-// 39.7 us (the weights at 4.8 TB/s).
+// Medians of a kernel trace: 4096 x 4096 x 8192 in 72.6 us (3.8 PFLOP/s; on
+// another card 82.8), 5120 x 11008 x 2048 in 80.2 us (2.9; 88.8), 1015 x 12288 x
+// 2048 / 2080 in 22.1 / 29.8 us, 128 x 7168 x 16384 in 21.4 us (18.0 without a
+// trace), 16 x 8 of 256 experts of 2048 x 2048 in 37.1 us (the weights at 5 TB/s).
+// What bounds them, as far as it is known. Power takes a fifth of the large
+// ones: on zeros the same launches take 55.8 instead of 69.6 us and 65.3 instead
+// of 83.1 us, and the clock, at 2.4 GHz on short kernels, falls to 1.8 .. 2.1 GHz;
+// the matrix cores are busy in 42% and 32% of the cycles. For 128 x 7168 x 16384
+// (11% of the cycles) the cause is not known: its time is the same on zeros, a
+// step's for rows of 8192 and 8320 bytes (318 and 319 ns), and its time with
+// eight stages instead of four or half the LDS reads (each wave one of a step's
+// instructions for the whole tile: 21.0 against 20.7 us); fewer lines of scales
+// are all that made it faster. Rows that start inside a cache line touch two
+// lines a step: the 29.8 us above.
 template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, int PATH, int Q>
 __global__ void __launch_bounds__(WM * WN * 64)
 mx_tile_kernel(MxGemmProblem p, int tiles_m, int tiles_n) {
@@ -870,7 +879,9 @@ hipError_t launch_skinny(const MxGemmProblem& p, hipStream_t stream) {
 
 // Tile I of its table. WM x WN waves and scales Q steps at a time where K is
 // whole steps, WM2 x WN2 and pairs otherwise (more registers: fewer, larger
-// waves keep two workgroups on a compute unit, or avoid spills).
+// waves keep two workgroups on a compute unit, or avoid spills). One instance
+// spills: 256 x 256 of whole steps needs two registers more than the 256 a lane
+// has; they are stored once before the K loop and loaded once behind it.
 template <int I, bool GROUPED, int WM, int WN, int STAGES, int Q = 2, int WM2 = WM, int WN2 = WN>
 hipError_t launch_tile(const MxGemmProblem& p, hipStream_t stream) {
     constexpr MxTile T = GROUPED ? kMxGrouped[I] : kMxDense[I];
@@ -927,6 +938,9 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream) {
     // Up to 16 rows, where 64-column tiles would fill under a third of the
     // compute units: 1 x 4096 x 7168 5.0 us against 8.0 us with the smallest
     // tile, 16 x 4096 x 7168 6.3 / 8.1 us (16 x 7168 x 16384: 20 / 15 us).
+    // Eight waves from K = 4096 on, four below: 1 x 4096 x 7168 5.15 us against
+    // 5.79, x 4096 3.62 / 3.72, x 2048 2.93 / 2.81, x 1024 2.55 / 2.42; 16 x 4096 x
+    // 7168 6.51 / 6.77, x 2048 3.33 / 3.21.
     if (p.M <= 16 && (uint64_t)p.N * 3 <= (uint64_t)p.cus * 64)
         return p.K >= 8 * 512 ? launch_skinny<8>(p, stream) : launch_skinny<4>(p, stream);
     switch (mx_dense_tile(p.M, p.N, p.K, p.cus)) {

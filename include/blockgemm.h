@@ -506,6 +506,11 @@ bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t
  * makes mean_probs and loss NaN; its ids and places stay valid. What the logits
  * of rows hold that valid leaves out changes nothing. Sums over rows are added in a fixed
  * order: repeated calls return identical bits.
+ * A probability is 2^((x - top) log2 e) over the row's sum, each operation in
+ * FP32: its relative error is at most about 2^-23 of |x - top| plus (E + 16)
+ * 2^-24. mean_probs and loss are FP32 sums of these over the rows, at most 2^-24
+ * of the value off per addition in a chain; the longest chain has fewer than
+ * 5000 + T / 65472 of them.
  *
  *  logits: [T, E] of logits_type, read.  valid: T bytes or NULL.
  *  out:    a host struct of device pointers, all required where their array is
@@ -516,6 +521,8 @@ bg_status gemm_mxfp4_grouped(const uint8_t* A, const uint8_t* SFA, const uint8_t
  *          initialization; calls that may run concurrently need separate ones.
  *  1 <= E <= 1024, 1 <= k <= min(E, 16), T * k < 2^31 (BG_ERR_SHAPE otherwise).
  *  T == 0 writes counts, offsets, mean_probs, loss and n_valid (zeros).
+ *  Time grows with T up to 16.7 million rows; beyond, a part of it (sums over
+ *  workgroups of 65472 rows) with T squared.
  */
 typedef struct bg_moe_routing {
     int32_t* ids;        /* [T, k]  */
