@@ -53,6 +53,13 @@ _SIGS = {
     "gemm_mxfp4_grouped": [_p, _p, _p, _p, _p, _p, _u32, _u32, _u32, _u32, _p],
     "moe_route": [_p, ctypes.c_int, _p, _p, _p, _sz, _u32, _u32, _u32, ctypes.c_int, _p],
     "moe_route_backward": [_p, ctypes.c_int, _p, _p, _p, _p, _p, _p, _p, _u32, _u32, _u32, ctypes.c_int, _p],
+    "gemm_bf16_gated": [_p, _p, _p, _p, _p, _p, ctypes.c_int, _u32, _u32, _u32, _p],
+    "gemm_bf16_gated_backward": [_p, _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _sz, _u32, _u32, _u32, _p],
+    "gemm_bf16_gated_backward_workspace": [_u32, _u32, _u32, _p],
+    "gemm_bf16_nn": [_p, _p, _p, _p, _sz, _u32, _u32, _u32, _p],
+    "gemm_bf16_tn": [_p, _p, _p, _p, _sz, _u32, _u32, _u32, _p],
+    "gemm_bf16_nn_workspace": [_u32, _u32, _u32, _p],
+    "gemm_bf16_tn_workspace": [_u32, _u32, _u32, _p],
 }
 for _name, _args in _SIGS.items():
     try:
@@ -733,6 +740,128 @@ def moe_route_backward(logits: torch.Tensor, routing: MoeRouting, dweights: torc
                                   _ptr(routing.n_valid), _ptr(dweights), _ptr(dloss), _ptr(out), t, e, routing.k,
                                   1 if routing.normalize else 0, _stream(stream)), "moe_route_backward")
     return out
+
+
+# ---------------------------------------------------------------------------
+# The gated MLP block, and the gradients of dense products
+# ---------------------------------------------------------------------------
+
+_ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}   # bg_activation
+
+
+def _activation(act: str) -> int:
+    kind = _ACTIVATIONS.get(act)
+    if kind is None:
+        raise ValueError(f"act must be one of {', '.join(map(repr, _ACTIVATIONS))}, got {act!r}")
+    return kind
+
+
+def _bytes_of(query, name: str, m: int, n: int, k: int) -> int:
+    nbytes = ctypes.c_size_t(0)
+    _check(query(m, n, k, ctypes.byref(nbytes)), name)
+    return nbytes.value
+
+
+def gemm_bf16_nn_workspace(m: int, n: int, k: int) -> int:
+    """Bytes of workspace gemm_bf16_nn needs on the current device."""
+    return _bytes_of(lib.gemm_bf16_nn_workspace, "gemm_bf16_nn_workspace", m, n, k)
+
+
+def gemm_bf16_tn_workspace(m: int, n: int, k: int) -> int:
+    """Bytes of workspace gemm_bf16_tn needs on the current device."""
+    return _bytes_of(lib.gemm_bf16_tn_workspace, "gemm_bf16_tn_workspace", m, n, k)
+
+
+def gemm_bf16_gated_backward_workspace(m: int, n: int, k: int) -> int:
+    """Bytes of workspace gemm_bf16_gated_backward needs on the current device."""
+    return _bytes_of(lib.gemm_bf16_gated_backward_workspace, "gemm_bf16_gated_backward_workspace", m, n, k)
+
+
+def _scratch(workspace, need, like: torch.Tensor, stream):
+    """(workspace, its bytes): the caller's, or a new one of need() bytes."""
+    if workspace is None:
+        nbytes = need()
+        if nbytes == 0:
+            return None, 0
+        return _new(like, nbytes, torch.uint8, stream), nbytes
+    return workspace, _tensor(workspace, "workspace").numel() * workspace.element_size()
+
+
+def _out(out, shape, like: torch.Tensor, stream, what: str = "out") -> torch.Tensor:
+    if out is None:
+        return _new(like, shape, torch.bfloat16, stream)
+    _shape(_bits16(out, what), shape, what)
+    return out
+
+
+def gemm_bf16_nn(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """C[M,N] = bf16(A[M,K] @ B[K,N]), FP32 accumulation: dX = dY @ W for weights W [out, in]. `workspace` is a
+    byte tensor of gemm_bf16_nn_workspace(M, N, K) bytes (allocated if None)."""
+    m, k = _dims(_bits16(a, "A"), 2, "A")
+    _, n = _dims(_bits16(b, "B"), 2, "B")
+    _shape(b, (k, n), "B")
+    _on_device(a, b, out, workspace)
+    out = _out(out, (m, n), a, stream)
+    workspace, ws_bytes = _scratch(workspace, lambda: gemm_bf16_nn_workspace(m, n, k), a, stream)
+    _check(lib.gemm_bf16_nn(_ptr(a), _ptr(b), _ptr(out), _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
+           "gemm_bf16_nn")
+    return out
+
+
+def gemm_bf16_tn(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """C[M,N] = bf16(A[K,M]^T @ B[K,N]), FP32 accumulation: dW = dY^T @ X, the sum over the rows of both.
+    `workspace` is a byte tensor of gemm_bf16_tn_workspace(M, N, K) bytes (allocated if None)."""
+    k, m = _dims(_bits16(a, "A"), 2, "A")
+    _, n = _dims(_bits16(b, "B"), 2, "B")
+    _shape(b, (k, n), "B")
+    _on_device(a, b, out, workspace)
+    out = _out(out, (m, n), a, stream)
+    workspace, ws_bytes = _scratch(workspace, lambda: gemm_bf16_tn_workspace(m, n, k), a, stream)
+    _check(lib.gemm_bf16_tn(_ptr(a), _ptr(b), _ptr(out), _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
+           "gemm_bf16_tn")
+    return out
+
+
+def gemm_bf16_gated(a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, act: str = "silu", save: bool = False,
+                    out: torch.Tensor | None = None, stream=None):
+    """H = bf16(act(A @ B0^T) * (A @ B1^T)) for A [M,K], B0 and B1 [N,K]; act is "silu" or "gelu_tanh". With
+    `save`, (H, G, U): G = bf16(A @ B0^T) and U = bf16(A @ B1^T) too, for gemm_bf16_gated_backward."""
+    kind = _activation(act)
+    m, k = _dims(_bits16(a, "A"), 2, "A")
+    n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
+    _shape(b0, (n, k), "B0")
+    _shape(_bits16(b1, "B1"), (n, k), "B1")
+    _on_device(a, b0, b1, out)
+    out = _out(out, (m, n), a, stream)
+    g, u = (_new(a, (m, n), torch.bfloat16, stream) for _ in range(2)) if save else (None, None)
+    _check(lib.gemm_bf16_gated(_ptr(a), _ptr(b0), _ptr(b1), _ptr(out), _ptr(g), _ptr(u), kind, m, n, k,
+                               _stream(stream)), "gemm_bf16_gated")
+    return (out, g, u) if save else out
+
+
+def gemm_bf16_gated_backward(dh: torch.Tensor, a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, g: torch.Tensor,
+                             u: torch.Tensor, act: str = "silu", need_a: bool = True, need_b: bool = True,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """(dA, dB0, dB1) for a gradient dH [M,N] of gemm_bf16_gated's H, with the G and U it saved; None where need_a
+    or need_b is false. `workspace` is a byte tensor of gemm_bf16_gated_backward_workspace(M, N, K) bytes (allocated
+    if None)."""
+    kind = _activation(act)
+    m, k = _dims(_bits16(a, "A"), 2, "A")
+    n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
+    _shape(b0, (n, k), "B0")
+    _shape(_bits16(b1, "B1"), (n, k), "B1")
+    for t, what in ((dh, "dH"), (g, "G"), (u, "U")):
+        _shape(_bits16(t, what), (m, n), what)
+    _on_device(dh, a, b0, b1, g, u, workspace)
+    da = _new(a, (m, k), torch.bfloat16, stream) if need_a else None
+    db0, db1 = (_new(a, (n, k), torch.bfloat16, stream) for _ in range(2)) if need_b else (None, None)
+    workspace, ws_bytes = _scratch(workspace, lambda: gemm_bf16_gated_backward_workspace(m, n, k), a, stream)
+    _check(lib.gemm_bf16_gated_backward(_ptr(dh), _ptr(a), _ptr(b0), _ptr(b1), _ptr(g), _ptr(u), _ptr(da), _ptr(db0),
+                                        _ptr(db1), kind, _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
+           "gemm_bf16_gated_backward")
+    return da, db0, db1
 
 
 # ---------------------------------------------------------------------------

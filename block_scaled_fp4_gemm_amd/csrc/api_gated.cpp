@@ -1,0 +1,203 @@
+// C ABI entry points of the gated MLP block and of the gradients of dense
+// products: argument validation, device check, kernel dispatch. As in api.cpp,
+// validation is plain host code and nothing is enqueued unless every check
+// passes.
+#include "api_checks.hpp"
+#include "bg_internal.hpp"
+#include "gated_tiles.hpp"
+
+namespace {
+
+using namespace bg;
+
+bool act_ok(int act) { return act == BG_SILU || act == BG_GELU_TANH; }
+
+// An operand of this size can exist: below 2^60 bytes, so that no byte count
+// and no address range wraps.
+bool fits(uint64_t rows, uint64_t cols, uint64_t size) {
+    return (unsigned __int128)rows * cols * size < ((unsigned __int128)1 << 60);
+}
+
+struct Operand {
+    const void* p;
+    uint64_t bytes;
+};
+
+// Pointers, alignment, and no output over an input or another output.
+template <size_t NI, size_t NO>
+bg_status check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
+    for (const Operand& o : in)
+        if (missing(o.p, o.bytes)) return BG_ERR_NULL;
+    for (const Operand& o : out)
+        if (missing(o.p, o.bytes)) return BG_ERR_NULL;
+    for (const Operand& o : in)
+        if (misaligned(o.p, o.bytes)) return BG_ERR_ALIGN;
+    for (const Operand& o : out)
+        if (misaligned(o.p, o.bytes)) return BG_ERR_ALIGN;
+    for (size_t i = 0; i < NO; ++i) {
+        const Range r = range_of(out[i].p, out[i].bytes);
+        for (const Operand& o : in)
+            if (overlap(r, range_of(o.p, o.bytes))) return BG_ERR_ALIAS;
+        for (size_t j = 0; j < i; ++j)
+            if (overlap(r, range_of(out[j].p, out[j].bytes))) return BG_ERR_ALIAS;
+    }
+    return BG_OK;
+}
+
+uint32_t pitch8(uint32_t n) { return (n + 7) / 8 * 8; }
+
+// An nn (C [M, N] of K terms, parts of them) or tn (parts outputs) product.
+GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t parts, uint32_t cus) {
+    return plan_of(false, M, N, tn ? K / 64 : K / 64 * parts, tn ? parts : 1, cus, tune(BG_TUNE_TILE));
+}
+uint64_t planes_bytes(const GatedPlan& p, uint32_t M, uint32_t N, uint32_t outputs) {
+    return p.splits > 1 ? (uint64_t)p.splits * outputs * M * N * 4 : 0;
+}
+
+bool transposed_shape_ok(bool tn, uint32_t M, uint32_t N, uint32_t K) {
+    return dims_ok(M, N, K) && N <= kMaxDim - 7 && M <= kMaxDim - 7 && fits(M, K, 2) && fits(K, N, 2) &&
+           fits(M, N, 64 * 4) && gated_launches(GatedPlan{GT_256x256, 1}, false, M, N, tn ? 2 : 1);
+}
+
+bg_status transposed_workspace(bool tn, uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
+    if (bytes == nullptr) return BG_ERR_NULL;
+    if (!transposed_shape_ok(tn, M, N, K)) return BG_ERR_SHAPE;
+    uint32_t cus = 0;
+    const bg_status s = check_device(&cus);
+    if (s != BG_OK) return s;
+    *bytes = M == 0 || N == 0 ? 0 : (size_t)planes_bytes(transposed_plan(tn, M, N, K, 1, cus), M, N, 1);
+    return BG_OK;
+}
+
+bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C, void* ws, size_t ws_bytes, uint32_t M,
+                     uint32_t N, uint32_t K, void* stream) {
+    if (!transposed_shape_ok(tn, M, N, K)) return BG_ERR_SHAPE;
+    if (M == 0 || N == 0) return BG_OK;
+    const Operand in[] = {{A, (uint64_t)M * K * 2}, {B, (uint64_t)K * N * 2}};
+    const Operand out[] = {{C, (uint64_t)M * N * 2}};
+    bg_status s = check_operands(in, out);
+    if (s != BG_OK) return s;
+    uint32_t cus = 0;
+    if ((s = check_device(&cus)) != BG_OK) return s;
+    const GatedPlan plan = transposed_plan(tn, M, N, K, 1, cus);
+    const uint64_t need = planes_bytes(plan, M, N, 1);
+    if (need != 0) {
+        if (ws == nullptr || ws_bytes < need) return BG_ERR_WORKSPACE;
+        const Operand with[] = {in[0], in[1], out[0]}, planes[] = {{ws, need}};
+        if ((s = check_operands(with, planes)) != BG_OK) return s;
+    }
+    return launched(launch_transposed(TransposedProblem{tn, A, nullptr, B, nullptr, C, nullptr, static_cast<float*>(ws), M, N, K,
+                                                        tn ? M : K, 1, plan.tile, plan.splits},
+                                      (hipStream_t)stream));
+}
+
+bool gated_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
+    return dims_ok(M, N, K) && N <= kMaxDim - 7 && M <= kMaxDim - 7 && K <= kMaxDim - 7 && fits(M, K, 2) && fits(N, K, 2) &&
+           fits(M, N, 2) && gated_launches(GatedPlan{GT_256x256, 1}, true, M, N, 1);
+}
+
+// The gradient's workspace: dG and dU, then the larger of the two products' planes.
+struct GradPlan {
+    GatedPlan nn, tn;
+    uint64_t half, bytes;    // of dG; of all
+};
+GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
+    GradPlan g;
+    g.nn = transposed_plan(false, M, K, N, 2, cus);
+    g.tn = transposed_plan(true, N, K, M, 2, cus);
+    g.half = (uint64_t)M * pitch8(N) * 2;
+    const uint64_t a = planes_bytes(g.nn, M, K, 1), b = planes_bytes(g.tn, N, K, 2);
+    g.bytes = 2 * g.half + (a > b ? a : b);
+    return g;
+}
+
+bool grad_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
+    return gated_shape_ok(M, N, K) && transposed_shape_ok(false, M, K, N) && transposed_shape_ok(true, N, K, M);
+}
+
+}  // namespace
+
+extern "C" {
+
+bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, uint16_t* G, uint16_t* U,
+                          int act, uint32_t M, uint32_t N, uint32_t K, void* stream) {
+    if (!gated_shape_ok(M, N, K) || !act_ok(act)) return BG_ERR_SHAPE;
+    if (M == 0 || N == 0) return BG_OK;
+    if ((G == nullptr) != (U == nullptr)) return BG_ERR_NULL;
+    const uint64_t b = (uint64_t)N * K * 2, c = (uint64_t)M * N * 2, kept = G != nullptr ? c : 0;
+    const Operand in[] = {{A, (uint64_t)M * K * 2}, {B0, b}, {B1, b}};
+    const Operand out[] = {{H, c}, {G, kept}, {U, kept}};
+    bg_status s = check_operands(in, out);
+    if (s != BG_OK) return s;
+    uint32_t cus = 0;
+    if ((s = check_device(&cus)) != BG_OK) return s;
+    const GatedPlan plan = plan_of(true, M, N, K / 64, 1, cus, tune(BG_TUNE_TILE));
+    return launched(launch_gated(GatedProblem{A, B0, B1, H, G, U, M, N, K, act, plan.tile}, (hipStream_t)stream));
+}
+
+bg_status gemm_bf16_nn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
+    return transposed_workspace(false, M, N, K, bytes);
+}
+bg_status gemm_bf16_tn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
+    return transposed_workspace(true, M, N, K, bytes);
+}
+
+bg_status gemm_bf16_nn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* workspace, size_t workspace_bytes, uint32_t M,
+                       uint32_t N, uint32_t K, void* stream) {
+    return transposed(false, A, B, C, workspace, workspace_bytes, M, N, K, stream);
+}
+bg_status gemm_bf16_tn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* workspace, size_t workspace_bytes, uint32_t M,
+                       uint32_t N, uint32_t K, void* stream) {
+    return transposed(true, A, B, C, workspace, workspace_bytes, M, N, K, stream);
+}
+
+bg_status gemm_bf16_gated_backward_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
+    if (bytes == nullptr) return BG_ERR_NULL;
+    if (!grad_shape_ok(M, N, K)) return BG_ERR_SHAPE;
+    uint32_t cus = 0;
+    const bg_status s = check_device(&cus);
+    if (s != BG_OK) return s;
+    *bytes = (size_t)grad_plan(M, N, K, cus).bytes;
+    return BG_OK;
+}
+
+bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const uint16_t* B0, const uint16_t* B1,
+                                   const uint16_t* G, const uint16_t* U, uint16_t* dA, uint16_t* dB0, uint16_t* dB1, int act,
+                                   void* workspace, size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, void* stream) {
+    if (!grad_shape_ok(M, N, K) || !act_ok(act)) return BG_ERR_SHAPE;
+    if ((dB0 == nullptr) != (dB1 == nullptr)) return BG_ERR_NULL;
+    const uint64_t a = (uint64_t)M * K * 2, b = (uint64_t)N * K * 2, c = (uint64_t)M * N * 2;
+    const Operand in[] = {{dH, c}, {A, dB0 != nullptr ? a : 0}, {B0, dA != nullptr ? b : 0}, {B1, dA != nullptr ? b : 0},
+                          {G, c}, {U, c}};
+    const Operand out[] = {{dA, dA != nullptr ? a : 0}, {dB0, dB0 != nullptr ? b : 0}, {dB1, dB1 != nullptr ? b : 0}};
+    bg_status s = check_operands(in, out);
+    if (s != BG_OK) return s;
+    uint32_t cus = 0;
+    if ((s = check_device(&cus)) != BG_OK) return s;
+    const GradPlan plan = grad_plan(M, N, K, cus);
+    if (plan.bytes != 0) {
+        if (workspace == nullptr || workspace_bytes < plan.bytes) return BG_ERR_WORKSPACE;
+        const Operand with[] = {in[0], in[1], in[2], in[3], in[4], in[5], out[0], out[1], out[2]}, ws[] = {{workspace, plan.bytes}};
+        if ((s = check_operands(with, ws)) != BG_OK) return s;
+    }
+    const hipStream_t st = (hipStream_t)stream;
+    uint16_t* dG = static_cast<uint16_t*>(workspace);
+    uint16_t* dU = dG + plan.half / 2;
+    float* planes = reinterpret_cast<float*>(dU + plan.half / 2);
+    const uint32_t ld = pitch8(N);
+    const bool want_a = dA != nullptr && M != 0 && K != 0, want_b = dB0 != nullptr && N != 0 && K != 0;
+    if (!want_a && !want_b) return BG_OK;
+    hipError_t e = hipSuccess;
+    if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, dG, dU, M, N, ld, act}, st);
+    if (e == hipSuccess && want_a)
+        e = launch_transposed(TransposedProblem{false, dG, dU, B0, B1, dA, nullptr, planes, M, K, N, ld, 2, plan.nn.tile,
+                                                plan.nn.splits},
+                              st);
+    if (e == hipSuccess && want_b)
+        e = launch_transposed(TransposedProblem{true, dG, dU, A, nullptr, dB0, dB1, planes, N, K, M, ld, 2, plan.tn.tile,
+                                                plan.tn.splits},
+                              st);
+    return launched(e);
+}
+
+}  // extern "C"

@@ -100,6 +100,36 @@ struct RouteBackwardProblem {
     int normalize;
 };
 
+struct GatedProblem {
+    const uint16_t* A;     // [M, K] bf16
+    const uint16_t *B0, *B1;   // [N, K]
+    uint16_t *H, *G, *U;   // [M, N]; G and U NULL where they are not kept
+    uint32_t M, N, K;
+    int act;               // bg_activation
+    int tile;              // GatedTile
+};
+
+// nn: C0 = A0 B0 (+ A1 B1 with parts == 2), A [M, K], B [K, N].
+// tn: C0 = A0^T B0 (and C1 = A1^T B0 with parts == 2), A [K, M], B [K, N].
+struct TransposedProblem {
+    bool tn;
+    const uint16_t *A0, *A1;
+    const uint16_t *B0, *B1;
+    uint16_t *C0, *C1;
+    float* planes;         // [splits][outputs][M][N], where splits > 1
+    uint32_t M, N, K;
+    uint32_t lda;          // elements between A's rows
+    uint32_t parts;
+    int tile, splits;      // GatedPlan
+};
+
+struct GateGradProblem {
+    const uint16_t *dH, *G, *U;   // [M, N]
+    uint16_t *dG, *dU;            // [M, ld], ld = N rounded up to a multiple of 8
+    uint32_t M, N, ld;
+    int act;
+};
+
 // Pieces of 512 elements (a wave's) of a row of mxfp4_quantize, which numbers those of all rows in 32 bits.
 constexpr uint32_t mx_quant_pieces(uint32_t K) { return K / 512 + (K % 512 != 0); }
 constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 bytes stay within 32-bit offsets
@@ -180,5 +210,10 @@ hipError_t launch_gemm_mxfp4(const MxGemmProblem& p, hipStream_t stream);
 // T may be 0 (the sums of an empty batch are still written).
 hipError_t launch_moe_route(const RouteProblem& p, hipStream_t stream);
 hipError_t launch_moe_route_backward(const RouteBackwardProblem& p, hipStream_t stream);
+
+
+hipError_t launch_gated(const GatedProblem& p, hipStream_t stream);
+hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream);
+hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t stream);
 
 }  // namespace bg

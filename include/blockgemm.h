@@ -564,6 +564,82 @@ bg_status moe_route_backward(const void* logits, int logits_type, const int32_t*
                              void* stream);
 
 /*
+ * The gated MLP block: act(A B0^T) * (A B1^T), elementwise, and its gradient.
+ *   silu:       act(g) = g s(g),                               s(z) = 1 / (1 + e^-z)
+ *   gelu_tanh:  act(g) = g s(2 sqrt(2 / pi) (g + 0.044715 g^3))   (the tanh form of gelu)
+ */
+typedef enum bg_activation { BG_SILU = 0, BG_GELU_TANH = 1 } bg_activation;
+
+/*
+ * gemm_bf16_gated: H[i,j] = bf16( act(g) * u ), g = sum_k A[i,k] B0[j,k], u = sum_k
+ * A[i,k] B1[j,k], both products of one pass over A, the activation and the
+ * product on the FP32 sums.
+ *
+ *  A: [M, K], B0, B1: [N, K] BF16, read.  H: [M, N] BF16, written.
+ *  G, U: both NULL, or [M, N] BF16, written: bf16(g) and bf16(u), which the
+ *     gradient takes. One of them alone is BG_ERR_NULL.
+ *  act: a bg_activation (BG_ERR_SHAPE otherwise).
+ *  K % 8 != 0 takes a slower guarded load path. The summation order is fixed by
+ *  the shape: repeated calls return identical bits. Outputs overlap neither an
+ *  input nor each other (BG_ERR_ALIAS). A launch's grid holds ceil(M / 256) *
+ *  ceil(N / 128) < 2^23 (BG_ERR_SHAPE otherwise).
+ */
+bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, uint16_t* G, uint16_t* U,
+                          int act, uint32_t M, uint32_t N, uint32_t K, void* stream);
+
+/*
+ * gemm_bf16_gated_backward: the gradients of gemm_bf16_gated for a gradient dH of
+ * its result:
+ *   dG = bf16(dH * u * act'(g)), dU = bf16(dH * act(g)), on g and u as they were kept;
+ *   dA = bf16(dG B0 + dU B1), dB0 = bf16(dG^T A), dB1 = bf16(dU^T A), FP32 sums.
+ *
+ *  dH, G, U: [M, N], A: [M, K], B0, B1: [N, K] BF16, read.
+ *  dA: [M, K] or NULL (not wanted; B0 and B1 are then not read).
+ *  dB0, dB1: [N, K], or both NULL (A is then not read).
+ *  workspace: device buffer of gemm_bf16_gated_backward_workspace(M, N, K) bytes,
+ *     16-byte aligned, not overlapping any operand (BG_ERR_WORKSPACE if missing
+ *     or smaller). It needs no initialization; calls that may run concurrently
+ *     need separate ones.
+ *  M == 0 gives dB0 = dB1 = 0, N == 0 gives dA = 0. Sizes as gemm_bf16_gated,
+ *  gemm_bf16_nn and gemm_bf16_tn for the three products.
+ */
+bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const uint16_t* B0, const uint16_t* B1,
+                                   const uint16_t* G, const uint16_t* U, uint16_t* dA, uint16_t* dB0, uint16_t* dB1, int act,
+                                   void* workspace, size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, void* stream);
+
+/* Bytes of workspace gemm_bf16_gated_backward needs on the current device, in
+ * *bytes (a tile override changes it: query after setting one). */
+bg_status gemm_bf16_gated_backward_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes);
+
+/*
+ * gemm_bf16_nn: C = bf16(A B), A [M, K], B [K, N], C [M, N]: the gradient dX = dY W
+ *   of a product Y = X W^T, with the weights as they lie.
+ * gemm_bf16_tn: C = bf16(A^T B), A [K, M], B [K, N], C [M, N]: its gradient dW =
+ *   dY^T X.
+ * FP32 accumulation in an order fixed by the shape: repeated calls return
+ * identical bits. Where the output has few tiles the reduction is split, and
+ * FP32 planes in the workspace are added in a fixed order.
+ *
+ *  workspace: device buffer of gemm_bf16_nn_workspace / gemm_bf16_tn_workspace
+ *     (M, N, K) bytes, 16-byte aligned, overlapping no operand; NULL where that
+ *     is 0 (BG_ERR_WORKSPACE if missing or smaller). It needs no initialization;
+ *     calls that may run concurrently need separate ones.
+ *  Rows of a pitch that is not a multiple of 16 bytes take a slower guarded load
+ *  path. C must not overlap an input (BG_ERR_ALIAS). A launch's grid holds
+ *  ceil(M / 256) * ceil(N / 256) < 2^23 for nn and half as many for tn
+ *  (BG_ERR_SHAPE otherwise).
+ */
+bg_status gemm_bf16_nn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* workspace, size_t workspace_bytes, uint32_t M,
+                       uint32_t N, uint32_t K, void* stream);
+bg_status gemm_bf16_tn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* workspace, size_t workspace_bytes, uint32_t M,
+                       uint32_t N, uint32_t K, void* stream);
+
+/* Bytes of workspace gemm_bf16_nn and gemm_bf16_tn need on the current device
+ * (0 where the reduction is not split), in *bytes. */
+bg_status gemm_bf16_nn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes);
+bg_status gemm_bf16_tn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes);
+
+/*
  * bf16_scaled_add: out[i] = bf16( f32(out[i]) + fl32(scale * f32(delta[i])) )
  * over `count` BF16 elements. The second half of the unfused LoRA fold that
  * gemm_bf16_scaled_acc must equal bit for bit (gemm_dense.rs page, doc comment

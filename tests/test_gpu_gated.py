@@ -1,0 +1,79 @@
+"""The gated block, its gradient and the transposed products against FP64."""
+import pytest
+import torch
+
+import block_scaled_fp4_gemm_amd as bg
+from gated_util import check_backward, check_gated, check_product, grid, normal
+from oracle import gated as og
+
+pytestmark = pytest.mark.gpu
+
+TILES = range(3)
+# one element, one row, less than a step, whole steps, odd everything, several
+# tiles of every size with ragged edges
+SHAPES = [(1, 1, 1), (1, 8, 8), (3, 130, 64), (64, 64, 64), (65, 127, 72), (128, 136, 128), (300, 200, 136),
+          (257, 513, 1000), (70, 1000, 251), (5, 2048, 2056)]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gated(m, n, k, act):
+    a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.5 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
+    h = bg.gemm_bf16_gated(a, b0, b1, act=act)
+    check_gated(h, a, b0, b1, act, f"{m}x{n}x{k} {act}")
+    h2, g, u = bg.gemm_bf16_gated(a, b0, b1, act=act, save=True)
+    assert torch.equal(h, h2)
+    check_product(g, a, b0.t(), "G")
+    check_product(u, a, b1.t(), "U")
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("m,n,k", [(3, 130, 64), (257, 300, 1000), (513, 261, 72), (300, 200, 131)])
+def test_every_tile_gives_the_same_bits(m, n, k, tile, force):
+    a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.0 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
+    bt = b0.t().contiguous()
+    at = a.t().contiguous()
+    want = bg.gemm_bf16_gated(a, b0, b1, save=True)
+    force(bg.TUNE_TILE, 16 + 0)
+    nn, tn = bg.gemm_bf16_nn(a, bt), bg.gemm_bf16_tn(at, bt)
+    force(bg.TUNE_TILE, 16 + tile)
+    for got, w in zip(bg.gemm_bf16_gated(a, b0, b1, save=True), want):
+        assert torch.equal(got, w)
+    assert torch.equal(bg.gemm_bf16_nn(a, bt), nn)
+    assert torch.equal(bg.gemm_bf16_tn(at, bt), tn)
+    check_product(nn, a, bt, "nn")
+    check_product(tn, a, bt, "tn")
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES + [(512, 264, 5000), (16, 64, 4096), (2048, 520, 64)])
+def test_transposed_products(m, n, k):
+    a, b = normal((m, k), 1.0, 1), normal((k, n), 1.0, 2)
+    check_product(bg.gemm_bf16_nn(a, b), a, b, f"nn {m}x{n}x{k}")
+    at = a.t().contiguous()
+    check_product(bg.gemm_bf16_tn(at, b), a, b, f"tn {m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("splits", [2, 3, 7])
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("m,n,k", [(130, 264, 1000), (64, 121, 448), (72, 128, 40)])
+def test_split_reduction_is_exact_on_whole_numbers(m, n, k, tile, splits, force):
+    a, b = grid((m, k), 1), grid((k, n), 2)
+    want = (a.double() @ b.double()).float().bfloat16()
+    force(bg.TUNE_TILE, 16 * splits + tile)
+    for _ in range(2):
+        assert torch.equal(bg.gemm_bf16_nn(a, b), want)
+        assert torch.equal(bg.gemm_bf16_tn(a.t().contiguous(), b), want)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("m,n,k", SHAPES + [(1030, 72, 64), (40, 3000, 136)])
+def test_backward(m, n, k, act):
+    a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.5 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
+    dh = normal((m, n), 0.01, 4)
+    _, g, u = bg.gemm_bf16_gated(a, b0, b1, act=act, save=True)
+    grads = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u, act=act)
+    check_backward(*grads, dh, a, b0, b1, g, u, act, f"{m}x{n}x{k} {act}")
+    da, n0, n1 = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u, act=act, need_b=False)
+    assert n0 is None and n1 is None and torch.equal(da, grads[0])
+    na, db0, db1 = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u, act=act, need_a=False)
+    assert na is None and torch.equal(db0, grads[1]) and torch.equal(db1, grads[2])
