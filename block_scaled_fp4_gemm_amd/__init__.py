@@ -60,6 +60,8 @@ _SIGS = {
     "gemm_bf16_tn": [_p, _p, _p, _p, _sz, _u32, _u32, _u32, _p],
     "gemm_bf16_nn_workspace": [_u32, _u32, _u32, _p],
     "gemm_bf16_tn_workspace": [_u32, _u32, _u32, _p],
+    "gemv_w4": [_p, _p, _p, _u32, _u32, _u32, _p],
+    "gemv_w4_gated": [_p, _p, _p, _p, ctypes.c_int, _u32, _u32, _u32, _p],
 }
 for _name, _args in _SIGS.items():
     try:
@@ -862,6 +864,77 @@ def gemm_bf16_gated_backward(dh: torch.Tensor, a: torch.Tensor, b0: torch.Tensor
                                         _ptr(db1), kind, _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
            "gemm_bf16_gated_backward")
     return da, db0, db1
+
+
+# ---------------------------------------------------------------------------
+# Few rows times weights in 4 bits
+# ---------------------------------------------------------------------------
+
+_W4_FORMATS = {"int4": 0, "mxfp4": 1, "nvfp4": 2}   # bg_w4_format
+_W4_GROUPS = {"mxfp4": 32, "nvfp4": 16}
+
+
+class W4Weights(NamedTuple):
+    """Weights [N, K] in 4 bits for gemv_w4 and gemv_w4_gated (see bg_w4 in include/blockgemm.h)."""
+    codes: torch.Tensor                    # bytes [N, K/2]
+    scales: torch.Tensor                   # [N, K/group]: bfloat16 for "int4", else bytes
+    format: str                            # "int4", "mxfp4" or "nvfp4"
+    group: int | None = None               # elements under a scale (None: the format's own)
+    zeros: torch.Tensor | None = None      # "int4": bytes [N, K/group], or None (8)
+    scale_2: float = 1.0                   # "nvfp4"
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("codes", _p), ("scales", _p), ("zeros", _p), ("format", ctypes.c_int), ("group", _u32), ("scale_2", ctypes.c_float)]
+
+
+def _w4(w: W4Weights, k: int, what: str):
+    """(struct, N, device tensors) of weights with K = k."""
+    kind = _W4_FORMATS.get(w.format)
+    if kind is None:
+        raise ValueError(f"{what}: format must be one of {', '.join(map(repr, _W4_FORMATS))}, got {w.format!r}")
+    own = _W4_GROUPS.get(w.format)
+    group = own if w.group is None else w.group
+    if group is None or group <= 0 or (group != own if own else group % 32 != 0):
+        raise ValueError(f"{what}: group of {w.format} weights must be {own or 'a multiple of 32'}, got {w.group}")
+    _blocks32(k)
+    if k % group != 0:
+        raise ValueError(f"{what}: K = {k} must be a multiple of the group, {group}")
+    n, _ = _dims(_bytes(w.codes, f"{what} codes"), 2, f"{what} codes")
+    _shape(w.codes, (n, k // 2), f"{what} codes")
+    scales = _bits16(w.scales, f"{what} scales") if own is None else _bytes(w.scales, f"{what} scales")
+    _shape(scales, (n, k // group), f"{what} scales")
+    if w.zeros is not None:
+        if own is not None:
+            raise ValueError(f"{what}: {w.format} weights have no zeros")
+        _shape(_bytes(w.zeros, f"{what} zeros"), (n, k // group), f"{what} zeros")
+    return _W4(_ptr(w.codes), _ptr(scales), _ptr(w.zeros), kind, group, w.scale_2), n, (w.codes, scales, w.zeros)
+
+
+def gemv_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, stream=None):
+    """Y[R,N] = bf16(x[R,K] @ deq(W)^T) for few rows of bfloat16 activations (16 at a time)."""
+    r, k = _dims(_bits16(x, "x"), 2, "x")
+    held, n, tensors = _w4(w, k, "W")
+    _on_device(x, *tensors, out)
+    out = _out(out, (r, n), x, stream)
+    _check(lib.gemv_w4(_ptr(x), ctypes.byref(held), _ptr(out), r, n, k, _stream(stream)), "gemv_w4")
+    return out
+
+
+def gemv_w4_gated(x: torch.Tensor, w0: W4Weights, w1: W4Weights, act: str = "silu", out: torch.Tensor | None = None,
+                  stream=None):
+    """H[R,N] = bf16(act(x @ deq(W0)^T) * (x @ deq(W1)^T)) for few rows; both weights of one format and group."""
+    kind = _activation(act)
+    r, k = _dims(_bits16(x, "x"), 2, "x")
+    held0, n, t0 = _w4(w0, k, "W0")
+    held1, n1, t1 = _w4(w1, k, "W1")
+    if n1 != n or held1.format != held0.format or held1.group != held0.group or (w0.zeros is None) != (w1.zeros is None):
+        raise ValueError("W0 and W1 must have the same shape, format and group, both or neither zeros")
+    _on_device(x, *t0, *t1, out)
+    out = _out(out, (r, n), x, stream)
+    _check(lib.gemv_w4_gated(_ptr(x), ctypes.byref(held0), ctypes.byref(held1), _ptr(out), kind, r, n, k,
+                             _stream(stream)), "gemv_w4_gated")
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -18,7 +18,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libblockgemm.so")
 OBJDIR = os.path.join(ROOT, "_build", "obj")
 
-SOURCES = ["api.cpp", "api_gated.cpp", "api_mx.cpp", "gemm_gated.hip", "gemm_mfma.hip", "gemm_ordered.hip", "moe_route.hip", "mxfp4.hip", "noalloc.hip"]
+SOURCES = ["api.cpp", "api_gated.cpp", "api_mx.cpp", "gemm_gated.hip", "gemm_mfma.hip", "gemm_ordered.hip", "gemv_w4.hip",
+           "moe_route.hip", "mxfp4.hip", "noalloc.hip"]
 
 ARCH = "gfx950"
 COMMON = [

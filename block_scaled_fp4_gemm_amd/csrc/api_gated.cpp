@@ -115,9 +115,66 @@ bool grad_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
     return gated_shape_ok(M, N, K) && transposed_shape_ok(false, M, K, N) && transposed_shape_ok(true, N, K, M);
 }
 
+// One set of weights in 4 bits: its shape, and its operands in order.
+bg_status check_w4(const bg_w4* w, uint32_t N, uint32_t K, Operand (&ops)[3]) {
+    if (w == nullptr) return BG_ERR_NULL;
+    uint64_t group = w->group, size = 1;
+    if (w->format == BG_W4_INT4) {
+        if (group == 0 || group % 32 != 0) return BG_ERR_SHAPE;
+        size = 2;
+    } else if (w->format == BG_W4_MXFP4 || w->format == BG_W4_NVFP4) {
+        if (w->zeros != nullptr) return BG_ERR_SHAPE;
+        if (group != (w->format == BG_W4_MXFP4 ? 32 : 16)) return BG_ERR_SHAPE;
+    } else {
+        return BG_ERR_SHAPE;
+    }
+    if (K % group != 0) return BG_ERR_SHAPE;
+    const uint64_t groups = (uint64_t)N * (K / group);
+    ops[0] = {w->codes, (uint64_t)N * (K / 2)};
+    ops[1] = {w->scales, groups * size};
+    ops[2] = {w->zeros, w->zeros != nullptr ? groups : 0};
+    return BG_OK;
+}
+
+bg_status gemv(const uint16_t* x, const bg_w4* w0, const bg_w4* w1, uint16_t* y, bool gated, int act, uint32_t R, uint32_t N,
+               uint32_t K, void* stream) {
+    if (!dims_ok(R, N, K) || K % 32 != 0 || R > kMaxGemvRows || !act_ok(act) || !fits(R, K, 2) || !fits(N, K, 2) ||
+        !fits(R, N, 2))
+        return BG_ERR_SHAPE;
+    // a launch holds fewer than 2^32 threads: 1024 for 16 columns and 16 rows at most
+    if (((uint64_t)N + 15) / 16 * (((uint64_t)R + 15) / 16) * 1024 >= ((uint64_t)1 << 32)) return BG_ERR_SHAPE;
+    Operand a[3] = {}, b[3] = {};
+    bg_status s = check_w4(w0, N, K, a);
+    if (s == BG_OK && gated) s = check_w4(w1, N, K, b);
+    if (s != BG_OK) return s;
+    if (gated && (w0->format != w1->format || w0->group != w1->group || (w0->zeros == nullptr) != (w1->zeros == nullptr)))
+        return BG_ERR_SHAPE;
+    if (R == 0 || N == 0) return BG_OK;
+    const Operand in[] = {{x, (uint64_t)R * K * 2}, a[0], a[1], a[2], b[0], b[1], b[2]};
+    const Operand out[] = {{y, (uint64_t)R * N * 2}};
+    if ((s = check_operands(in, out)) != BG_OK) return s;
+    uint32_t cus = 0;
+    if ((s = check_device(&cus)) != BG_OK) return s;
+    auto operand = [](const bg_w4* w) {
+        return W4Operand{w->codes, static_cast<const uint8_t*>(w->scales), w->zeros, w->scale_2};
+    };
+    return launched(launch_gemv_w4(GemvProblem{x, {operand(w0), gated ? operand(w1) : W4Operand{}}, y, R, N, K, w0->group,
+                                               w0->format, gated, act, cus},
+                                   (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
+
+bg_status gemv_w4(const uint16_t* X, const bg_w4* W, uint16_t* Y, uint32_t R, uint32_t N, uint32_t K, void* stream) {
+    return gemv(X, W, nullptr, Y, false, BG_SILU, R, N, K, stream);
+}
+
+bg_status gemv_w4_gated(const uint16_t* X, const bg_w4* W0, const bg_w4* W1, uint16_t* H, int act, uint32_t R, uint32_t N,
+                        uint32_t K, void* stream) {
+    return gemv(X, W0, W1, H, true, act, R, N, K, stream);
+}
 
 bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, uint16_t* G, uint16_t* U,
                           int act, uint32_t M, uint32_t N, uint32_t K, void* stream) {

@@ -130,9 +130,28 @@ struct GateGradProblem {
     int act;
 };
 
+struct W4Operand {
+    const uint8_t* codes;  // [N, K/2]
+    const uint8_t* scales; // int4: [N, K/group] bf16; mxfp4: [N, K/32]; nvfp4: [N, K/16]
+    const uint8_t* zeros;  // int4: [N, K/group], or NULL (8)
+    float scale_2;         // nvfp4
+};
+
+struct GemvProblem {
+    const uint16_t* x;     // [R, K] bf16
+    W4Operand w[2];        // the second where gated
+    uint16_t* y;           // [R, N] bf16
+    uint32_t R, N, K, group;
+    int format;            // bg_w4_format
+    bool gated;
+    int act;
+    uint32_t cus;
+};
+
 // Pieces of 512 elements (a wave's) of a row of mxfp4_quantize, which numbers those of all rows in 32 bits.
 constexpr uint32_t mx_quant_pieces(uint32_t K) { return K / 512 + (K % 512 != 0); }
 constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 bytes stay within 32-bit offsets
+constexpr uint32_t kMaxGemvRows = 1u << 16;   // sixteen rows of a grid's y
 constexpr uint32_t kMaxExperts = 1024;   // routing and grouped products
 constexpr uint32_t kMaxTopK = 16;
 
@@ -215,5 +234,6 @@ hipError_t launch_moe_route_backward(const RouteBackwardProblem& p, hipStream_t 
 hipError_t launch_gated(const GatedProblem& p, hipStream_t stream);
 hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream);
 hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t stream);
+hipError_t launch_gemv_w4(const GemvProblem& p, hipStream_t stream);
 
 }  // namespace bg

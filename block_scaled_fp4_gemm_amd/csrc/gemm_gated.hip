@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "bg_internal.hpp"
+#include "gate.hpp"
 #include "gated_tiles.hpp"
 #include "mma_common.hpp"
 #include "tile_order.hpp"
@@ -219,26 +220,6 @@ __device__ __forceinline__ void mma(const bf16x8 (&fa)[FM], const bf16x8 (&fb)[F
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-}
-
-// act(g) = g s(z(g)), s(z) = 1 / (1 + e^-z). Silu: z = g; gelu (tanh form): z =
-// 2 sqrt(2 / pi) (g + 0.044715 g^3). e^-z is one exp2, whose argument rounds
-// twice (2^-23 of |z|), so s is off by 2^-23 (|z| + 2) of its value: far below
-// half a BF16 step, 2^-9. Past z = -88.7 e^-z overflows and s is 0, where act(g)
-// is below 2^-121 and would be 0 or the smallest numbers of BF16.
-constexpr float kLog2e = 1.44269504f;
-constexpr float kGeluC = 1.59576912f;         // 2 sqrt(2 / pi)
-constexpr float kGeluK = 0.044715f;
-
-template <int ACT>
-__device__ __forceinline__ float gate_sigmoid(float g) {
-    const float z = ACT == BG_SILU ? g : kGeluC * __builtin_fmaf(kGeluK * g * g, g, g);
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -kLog2e));
-}
-
-template <int ACT>
-__device__ __forceinline__ float gate(float g) {
-    return g * gate_sigmoid<ACT>(g);
 }
 
 // Writes rows of bf16 (or FP32) results from the accumulators through LDS:

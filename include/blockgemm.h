@@ -640,6 +640,52 @@ bg_status gemm_bf16_nn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* byt
 bg_status gemm_bf16_tn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes);
 
 /*
+ * Weights [N, K] in 4 bits, two codes a byte (element 2t in the LOW nibble), with
+ * one scale for every `group` consecutive elements of a row; K % group == 0.
+ *   BG_W4_INT4:  s (q - z): q the code 0 .. 15, s BF16, z a byte (8 where zeros is
+ *                NULL); group a multiple of 32
+ *   BG_W4_MXFP4: e2m1(q) 2^(s - 127): s an E8M0 byte (255 = NaN), group 32
+ *   BG_W4_NVFP4: scale_2 e2m1(q) s: s an E4M3FN byte, group 16
+ * A host struct of device pointers; zeros NULL and scale_2 unused where the
+ * format has none.
+ */
+typedef enum bg_w4_format { BG_W4_INT4 = 0, BG_W4_MXFP4 = 1, BG_W4_NVFP4 = 2 } bg_w4_format;
+
+typedef struct bg_w4 {
+    const uint8_t* codes;  /* [N, K/2] */
+    const void* scales;    /* [N, K/group], BF16 (INT4) or bytes */
+    const uint8_t* zeros;  /* [N, K/group] or NULL */
+    int format;            /* bg_w4_format */
+    uint32_t group;
+    float scale_2;
+} bg_w4;
+
+/*
+ * gemv_w4: Y[r,n] = bf16( sum_k X[r,k] w[n,k] ) for few rows, BF16 activations and
+ * weights in 4 bits. Weights enter exactly, sums are FP32 in a fixed order:
+ * repeated calls return identical bits, and a row's bits do not depend on the
+ * other rows.
+ *
+ *  X: [R, K] BF16, read.  W: the weights [N, K].  Y: [R, N] BF16, written; must not
+ *  overlap an input (BG_ERR_ALIAS).
+ *  Made for up to 16 rows; more are taken 16 at a time, the weights read again
+ *  for each (R <= 65536). K % 32 == 0 and a grid of ceil(N / 16) * ceil(R / 16) <
+ *  2^22 (BG_ERR_SHAPE otherwise). All pointers 16-byte aligned (BG_ERR_ALIGN).
+ *  INT4: s (sum (16 + q) x - (16 + z) sum x) per group, so an infinity in a row of X
+ *  makes that row of Y NaN.
+ */
+bg_status gemv_w4(const uint16_t* X, const bg_w4* W, uint16_t* Y, uint32_t R, uint32_t N, uint32_t K, void* stream);
+
+/*
+ * gemv_w4_gated: the gated MLP block of few rows, H[r,n] = bf16( act(g) u ), g and u
+ * the FP32 sums of gemv_w4 for W0 and W1 (as gemm_bf16_gated). Both weights of
+ * one format and group, both or neither with zeros (BG_ERR_SHAPE otherwise).
+ * Other rules as gemv_w4.
+ */
+bg_status gemv_w4_gated(const uint16_t* X, const bg_w4* W0, const bg_w4* W1, uint16_t* H, int act, uint32_t R, uint32_t N,
+                        uint32_t K, void* stream);
+
+/*
  * bf16_scaled_add: out[i] = bf16( f32(out[i]) + fl32(scale * f32(delta[i])) )
  * over `count` BF16 elements. The second half of the unfused LoRA fold that
  * gemm_bf16_scaled_acc must equal bit for bit (gemm_dense.rs page, doc comment
