@@ -53,8 +53,9 @@ _SIGS = {
     "gemm_mxfp4_grouped": [_p, _p, _p, _p, _p, _p, _u32, _u32, _u32, _u32, _p],
     "moe_route": [_p, ctypes.c_int, _p, _p, _p, _sz, _u32, _u32, _u32, ctypes.c_int, _p],
     "moe_route_backward": [_p, ctypes.c_int, _p, _p, _p, _p, _p, _p, _p, _u32, _u32, _u32, ctypes.c_int, _p],
-    "gemm_bf16_gated": [_p, _p, _p, _p, _p, _p, ctypes.c_int, _u32, _u32, _u32, _p],
-    "gemm_bf16_gated_backward": [_p, _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _sz, _u32, _u32, _u32, _p],
+    "gemm_bf16_gated": [_p, _p, _p, _p, _p, _p, ctypes.c_int, ctypes.c_int, _u32, _u32, _u32, _p],
+    "gemm_bf16_gated_backward": [_p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _p, _p, ctypes.c_int, _p, _sz, _u32, _u32, _u32,
+                                 _p],
     "gemm_bf16_gated_backward_workspace": [_u32, _u32, _u32, _p],
     "gemm_bf16_nn": [_p, _p, _p, _p, _sz, _u32, _u32, _u32, _p],
     "gemm_bf16_tn": [_p, _p, _p, _p, _sz, _u32, _u32, _u32, _p],
@@ -826,10 +827,11 @@ def gemm_bf16_tn(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | None = No
     return out
 
 
-def gemm_bf16_gated(a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, act: str = "silu", save: bool = False,
-                    out: torch.Tensor | None = None, stream=None):
+def gemm_bf16_gated(a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, act: str = "silu",
+                    save: bool | torch.dtype = False, out: torch.Tensor | None = None, stream=None):
     """H = bf16(act(A @ B0^T) * (A @ B1^T)) for A [M,K], B0 and B1 [N,K]; act is "silu" or "gelu_tanh". With
-    `save`, (H, G, U): G = bf16(A @ B0^T) and U = bf16(A @ B1^T) too, for gemm_bf16_gated_backward."""
+    `save`, (H, G, U): G = A @ B0^T and U = A @ B1^T too, for gemm_bf16_gated_backward, in float32 (True) or in
+    the dtype given (torch.bfloat16: half the memory, the gradient a little less exact)."""
     kind = _activation(act)
     m, k = _dims(_bits16(a, "A"), 2, "A")
     n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
@@ -837,8 +839,10 @@ def gemm_bf16_gated(a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, act: st
     _shape(_bits16(b1, "B1"), (n, k), "B1")
     _on_device(a, b0, b1, out)
     out = _out(out, (m, n), a, stream)
-    g, u = (_new(a, (m, n), torch.bfloat16, stream) for _ in range(2)) if save else (None, None)
-    _check(lib.gemm_bf16_gated(_ptr(a), _ptr(b0), _ptr(b1), _ptr(out), _ptr(g), _ptr(u), kind, m, n, k,
+    kept = torch.float32 if save is True else save
+    g, u = (_new(a, (m, n), kept, stream) for _ in range(2)) if save else (None, None)
+    _check(lib.gemm_bf16_gated(_ptr(a), _ptr(b0), _ptr(b1), _ptr(out), _ptr(g), _ptr(u), _type(g, "save") if save else 0,
+                               kind, m, n, k,
                                _stream(stream)), "gemm_bf16_gated")
     return (out, g, u) if save else out
 
@@ -854,14 +858,18 @@ def gemm_bf16_gated_backward(dh: torch.Tensor, a: torch.Tensor, b0: torch.Tensor
     n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
     _shape(b0, (n, k), "B0")
     _shape(_bits16(b1, "B1"), (n, k), "B1")
-    for t, what in ((dh, "dH"), (g, "G"), (u, "U")):
-        _shape(_bits16(t, what), (m, n), what)
+    _shape(_bits16(dh, "dH"), (m, n), "dH")
+    kept = _type(g, "G")
+    _shape(g, (m, n), "G")
+    if _type(u, "U") != kept:
+        raise TypeError(f"U: expected {g.dtype}, got {u.dtype}")
+    _shape(u, (m, n), "U")
     _on_device(dh, a, b0, b1, g, u, workspace)
     da = _new(a, (m, k), torch.bfloat16, stream) if need_a else None
     db0, db1 = (_new(a, (n, k), torch.bfloat16, stream) for _ in range(2)) if need_b else (None, None)
     workspace, ws_bytes = _scratch(workspace, lambda: gemm_bf16_gated_backward_workspace(m, n, k), a, stream)
-    _check(lib.gemm_bf16_gated_backward(_ptr(dh), _ptr(a), _ptr(b0), _ptr(b1), _ptr(g), _ptr(u), _ptr(da), _ptr(db0),
-                                        _ptr(db1), kind, _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
+    _check(lib.gemm_bf16_gated_backward(_ptr(dh), _ptr(a), _ptr(b0), _ptr(b1), _ptr(g), _ptr(u), kept, _ptr(da),
+                                        _ptr(db0), _ptr(db1), kind, _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
            "gemm_bf16_gated_backward")
     return da, db0, db1
 

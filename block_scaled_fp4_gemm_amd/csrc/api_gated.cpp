@@ -10,6 +10,8 @@ namespace {
 
 using namespace bg;
 
+uint64_t type_size(int type) { return type == BG_BF16 ? 2 : 4; }
+bool type_ok(int type) { return type == BG_BF16 || type == BG_F32; }
 bool act_ok(int act) { return act == BG_SILU || act == BG_GELU_TANH; }
 
 // An operand of this size can exist: below 2^60 bytes, so that no byte count
@@ -93,7 +95,7 @@ bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C,
 
 bool gated_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
     return dims_ok(M, N, K) && N <= kMaxDim - 7 && M <= kMaxDim - 7 && K <= kMaxDim - 7 && fits(M, K, 2) && fits(N, K, 2) &&
-           fits(M, N, 2) && gated_launches(GatedPlan{GT_256x256, 1}, true, M, N, 1);
+           fits(M, N, 4) && gated_launches(GatedPlan{GT_256x256, 1}, true, M, N, 1);
 }
 
 // The gradient's workspace: dG and dU, then the larger of the two products' planes.
@@ -176,12 +178,12 @@ bg_status gemv_w4_gated(const uint16_t* X, const bg_w4* W0, const bg_w4* W1, uin
     return gemv(X, W0, W1, H, true, act, R, N, K, stream);
 }
 
-bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, uint16_t* G, uint16_t* U,
-                          int act, uint32_t M, uint32_t N, uint32_t K, void* stream) {
-    if (!gated_shape_ok(M, N, K) || !act_ok(act)) return BG_ERR_SHAPE;
+bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, void* G, void* U,
+                          int kept_type, int act, uint32_t M, uint32_t N, uint32_t K, void* stream) {
+    if (!gated_shape_ok(M, N, K) || !act_ok(act) || !type_ok(kept_type)) return BG_ERR_SHAPE;
     if (M == 0 || N == 0) return BG_OK;
     if ((G == nullptr) != (U == nullptr)) return BG_ERR_NULL;
-    const uint64_t b = (uint64_t)N * K * 2, c = (uint64_t)M * N * 2, kept = G != nullptr ? c : 0;
+    const uint64_t b = (uint64_t)N * K * 2, c = (uint64_t)M * N * 2, kept = G != nullptr ? (uint64_t)M * N * type_size(kept_type) : 0;
     const Operand in[] = {{A, (uint64_t)M * K * 2}, {B0, b}, {B1, b}};
     const Operand out[] = {{H, c}, {G, kept}, {U, kept}};
     bg_status s = check_operands(in, out);
@@ -189,7 +191,7 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
     uint32_t cus = 0;
     if ((s = check_device(&cus)) != BG_OK) return s;
     const GatedPlan plan = plan_of(true, M, N, K / 64, 1, cus, tune(BG_TUNE_TILE));
-    return launched(launch_gated(GatedProblem{A, B0, B1, H, G, U, M, N, K, act, plan.tile}, (hipStream_t)stream));
+    return launched(launch_gated(GatedProblem{A, B0, B1, H, G, U, kept_type, M, N, K, act, plan.tile}, (hipStream_t)stream));
 }
 
 bg_status gemm_bf16_nn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
@@ -219,13 +221,14 @@ bg_status gemm_bf16_gated_backward_workspace(uint32_t M, uint32_t N, uint32_t K,
 }
 
 bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const uint16_t* B0, const uint16_t* B1,
-                                   const uint16_t* G, const uint16_t* U, uint16_t* dA, uint16_t* dB0, uint16_t* dB1, int act,
-                                   void* workspace, size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, void* stream) {
-    if (!grad_shape_ok(M, N, K) || !act_ok(act)) return BG_ERR_SHAPE;
+                                   const void* G, const void* U, int kept_type, uint16_t* dA, uint16_t* dB0, uint16_t* dB1,
+                                   int act, void* workspace, size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, void* stream) {
+    if (!grad_shape_ok(M, N, K) || !act_ok(act) || !type_ok(kept_type)) return BG_ERR_SHAPE;
     if ((dB0 == nullptr) != (dB1 == nullptr)) return BG_ERR_NULL;
-    const uint64_t a = (uint64_t)M * K * 2, b = (uint64_t)N * K * 2, c = (uint64_t)M * N * 2;
+    const uint64_t a = (uint64_t)M * K * 2, b = (uint64_t)N * K * 2, c = (uint64_t)M * N * 2,
+                   kept = (uint64_t)M * N * type_size(kept_type);
     const Operand in[] = {{dH, c}, {A, dB0 != nullptr ? a : 0}, {B0, dA != nullptr ? b : 0}, {B1, dA != nullptr ? b : 0},
-                          {G, c}, {U, c}};
+                          {G, kept}, {U, kept}};
     const Operand out[] = {{dA, dA != nullptr ? a : 0}, {dB0, dB0 != nullptr ? b : 0}, {dB1, dB1 != nullptr ? b : 0}};
     bg_status s = check_operands(in, out);
     if (s != BG_OK) return s;
@@ -245,7 +248,7 @@ bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const 
     const bool want_a = dA != nullptr && M != 0 && K != 0, want_b = dB0 != nullptr && N != 0 && K != 0;
     if (!want_a && !want_b) return BG_OK;
     hipError_t e = hipSuccess;
-    if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, dG, dU, M, N, ld, act}, st);
+    if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, kept_type, dG, dU, M, N, ld, act}, st);
     if (e == hipSuccess && want_a)
         e = launch_transposed(TransposedProblem{false, dG, dU, B0, B1, dA, nullptr, planes, M, K, N, ld, 2, plan.nn.tile,
                                                 plan.nn.splits},

@@ -103,7 +103,9 @@ struct RouteBackwardProblem {
 struct GatedProblem {
     const uint16_t* A;     // [M, K] bf16
     const uint16_t *B0, *B1;   // [N, K]
-    uint16_t *H, *G, *U;   // [M, N]; G and U NULL where they are not kept
+    uint16_t* H;           // [M, N] bf16
+    void *G, *U;           // [M, N] of kept, or NULL where they are not kept
+    int kept;              // bg_type
     uint32_t M, N, K;
     int act;               // bg_activation
     int tile;              // GatedTile
@@ -124,8 +126,10 @@ struct TransposedProblem {
 };
 
 struct GateGradProblem {
-    const uint16_t *dH, *G, *U;   // [M, N]
-    uint16_t *dG, *dU;            // [M, ld], ld = N rounded up to a multiple of 8
+    const uint16_t* dH;    // [M, N] bf16
+    const void *G, *U;     // [M, N] of kept
+    int kept;              // bg_type
+    uint16_t *dG, *dU;     // [M, ld] bf16, ld = N rounded up to a multiple of 8
     uint32_t M, N, ld;
     int act;
 };

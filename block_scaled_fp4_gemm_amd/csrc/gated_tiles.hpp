@@ -7,11 +7,12 @@
 
 namespace bg {
 
-enum GatedTile : int { GT_256x256, GT_128x128, GT_64x128, GT_TILES };
+enum GatedTile : int { GT_256x256, GT_160x256, GT_256x128, GT_128x256, GT_128x128, GT_128x128_3, GT_64x128, GT_TILES };
 struct GatedTileSize {
     int bm, bn, threads;
 };
-constexpr GatedTileSize kGatedTiles[GT_TILES] = {{256, 256, 512}, {128, 128, 256}, {64, 128, 256}};
+constexpr GatedTileSize kGatedTiles[GT_TILES] = {{256, 256, 512}, {160, 256, 256}, {256, 128, 512}, {128, 256, 512},
+                                                     {128, 128, 256}, {128, 128, 256}, {64, 128, 256}};
 
 // Output columns of a tile of bn operand rows: a gated tile holds both products.
 constexpr int tile_columns(int bn, bool gated) { return gated ? bn / 2 : bn; }

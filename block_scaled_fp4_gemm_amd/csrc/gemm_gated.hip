@@ -50,7 +50,8 @@ struct GatedParams {
     // (and A1^T B0 -> C1 where parts == 2).
     const uint16_t *A0, *A1, *B0, *B1;
     void *C0, *C1;          // bf16, or FP32 planes in C0 (splits > 1)
-    uint16_t *G, *U;        // gated: the products themselves, or NULL
+    void *G, *U;            // gated: the products themselves, or NULL
+    int kept;               // bg_type of G and U
     int M, N, K;            // of one product
     int lda, ldb;           // elements between rows as they lie in memory
     int tiles_m, tiles_n;   // of one product
@@ -225,7 +226,7 @@ __device__ __forceinline__ void mma(const bf16x8 (&fa)[FM], const bf16x8 (&fb)[F
 // Writes rows of bf16 (or FP32) results from the accumulators through LDS:
 // whole rows, 16 contiguous bytes per lane. value(i, j, e) is element e of
 // 16 of fragment (i, j), JN fragments a wave, TNO columns a wave.
-template <typename OUT, int BM, int BNO, int WM, int WN, int FM, int JN, int NT, int CAP, class Value>
+template <typename OUT, bool STREAM, int BM, int BNO, int WM, int WN, int FM, int JN, int NT, int CAP, class Value>
 __device__ __forceinline__ void store_tile(OUT* C, int64_t ldc, int M, int N, int m0, int n0, uint8_t* lds, int wm,
                                            int wn, int lane, int tid, Value&& value) {
     constexpr int ELEM = sizeof(OUT), ROWB = BNO * ELEM, CPR = ROWB / 16, EPC = 16 / ELEM;
@@ -268,8 +269,8 @@ __device__ __forceinline__ void store_tile(OUT* C, int64_t ldc, int M, int N, in
             const u32x4 w = *reinterpret_cast<const u32x4*>(lds + slot(row, chunk));
             OUT* dst = C + (int64_t)m * ldc + n;
             if (n + EPC <= N) {
-                // BF16 results are not read again by this launch; planes are, by the next
-                if (aligned && ELEM == 2)
+                // results are not read again by this launch; planes are, by the next
+                if (aligned && STREAM)
                     __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(dst));
                 else
                     *reinterpret_cast<u32x4_any*>(dst) = w;
@@ -451,13 +452,20 @@ gated_kernel(GatedParams p) {
     uint8_t* lds = reinterpret_cast<uint8_t*>(smem);
     constexpr int CAP = STAGES * STAGE * 2;
     if constexpr (PAIR) {
-        auto out = [&](uint16_t* dst, auto&& value) {
-            store_tile<uint16_t, BM, BNO, WM, WN, FM, FN / 2, NT, CAP>(dst, p.N, p.M, p.N, m0, n0, lds, wm, wn, elane, etid,
-                                                                      value);
+        auto out = [&](auto* dst, auto&& value) {
+            store_tile<std::remove_reference_t<decltype(*dst)>, true, BM, BNO, WM, WN, FM, FN / 2, NT, CAP>(
+                dst, p.N, p.M, p.N, m0, n0, lds, wm, wn, elane, etid, value);
         };
         if (p.G != nullptr) {
-            out(p.G, [&](int i, int j, int e) { return acc[i][2 * j][e]; });
-            out(p.U, [&](int i, int j, int e) { return acc[i][2 * j + 1][e]; });
+            auto g = [&](int i, int j, int e) { return acc[i][2 * j][e]; };
+            auto u = [&](int i, int j, int e) { return acc[i][2 * j + 1][e]; };
+            if (p.kept == BG_F32) {
+                out(static_cast<float*>(p.G), g);
+                out(static_cast<float*>(p.U), u);
+            } else {
+                out(static_cast<uint16_t*>(p.G), g);
+                out(static_cast<uint16_t*>(p.U), u);
+            }
         }
         out(static_cast<uint16_t*>(C), [&](int i, int j, int e) { return gate<ACT>(acc[i][2 * j][e]) * acc[i][2 * j + 1][e]; });
     } else {
@@ -466,9 +474,9 @@ gated_kernel(GatedParams p) {
             const int64_t rows = MODE == MODE_TN ? (int64_t)p.M * p.parts : p.M;
             float* plane = static_cast<float*>(p.C0) + (int64_t)blockIdx.y * rows * p.N;
             if (MODE == MODE_TN && C != p.C0) plane += (int64_t)p.M * p.N;
-            store_tile<float, BM, BNO, WM, WN, FM, FN, NT, CAP>(plane, p.N, p.M, p.N, m0, n0, lds, wm, wn, elane, etid, value);
+            store_tile<float, false, BM, BNO, WM, WN, FM, FN, NT, CAP>(plane, p.N, p.M, p.N, m0, n0, lds, wm, wn, elane, etid, value);
         } else {
-            store_tile<uint16_t, BM, BNO, WM, WN, FM, FN, NT, CAP>(static_cast<uint16_t*>(C), p.N, p.M, p.N, m0, n0, lds, wm,
+            store_tile<uint16_t, true, BM, BNO, WM, WN, FM, FN, NT, CAP>(static_cast<uint16_t*>(C), p.N, p.M, p.N, m0, n0, lds, wm,
                                                                   wn, elane, etid, value);
         }
     }
@@ -487,26 +495,50 @@ __device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg,
     dg = dh * u * __builtin_fmaf(g * slope, s * (1.0f - s), s);
 }
 
-template <int ACT>
+// Eight values p[at ..] of which those below n exist.
+template <bool F32>
+__device__ __forceinline__ void kept8(const void* p, int64_t at, int n, float (&v)[8]) {
+    if constexpr (F32) {
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+        const float* q = static_cast<const float*>(p) + at;
+        if (n >= 8) {
+            const f32x4 a = *reinterpret_cast<const f32x4_any*>(q), b = *reinterpret_cast<const f32x4_any*>(q + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = a[e], v[e + 4] = b[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? q[e] : 0.0f;
+        }
+    } else {
+        const u32x4 w = guarded8(static_cast<const uint16_t*>(p) + at, n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+    }
+}
+
+template <int ACT, bool F32>
 __global__ void __launch_bounds__(256)
-gate_grad_kernel(const uint16_t* dH, const uint16_t* G, const uint16_t* U, uint16_t* dG, uint16_t* dU, int64_t chunks,
-                 int N, int ld) {
+gate_grad_kernel(GateGradProblem p, int64_t chunks) {
+    const int per = (int)(p.ld / 8);
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < chunks; q += (int64_t)gridDim.x * 256) {
-        const int64_t row = q / (ld / 8);
-        const int n = (int)(q - row * (ld / 8)) * 8;
-        const int64_t at = row * N + n;
-        const u32x4 h = guarded8(dH + at, N - n), g = guarded8(G + at, N - n), u = guarded8(U + at, N - n);
+        const int64_t row = q / per;
+        const int n = (int)(q - row * per) * 8, left = (int)p.N - n;
+        const int64_t at = row * p.N + n;
+        float h[8], g[8], u[8];
+        kept8<false>(p.dH, at, left, h);
+        kept8<F32>(p.G, at, left, g);
+        kept8<F32>(p.U, at, left, u);
         u32x4 og, ou;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float g0, g1, u0, u1;
-            gate_grad<ACT>(bf16_lo(h[e]), bf16_lo(g[e]), bf16_lo(u[e]), g0, u0);
-            gate_grad<ACT>(bf16_hi(h[e]), bf16_hi(g[e]), bf16_hi(u[e]), g1, u1);
+            gate_grad<ACT>(h[2 * e], g[2 * e], u[2 * e], g0, u0);
+            gate_grad<ACT>(h[2 * e + 1], g[2 * e + 1], u[2 * e + 1], g1, u1);
             og[e] = pack_bf16x2(g0, g1);
             ou[e] = pack_bf16x2(u0, u1);
         }
-        *reinterpret_cast<u32x4*>(dG + row * ld + n) = og;
-        *reinterpret_cast<u32x4*>(dU + row * ld + n) = ou;
+        *reinterpret_cast<u32x4*>(p.dG + row * p.ld + n) = og;
+        *reinterpret_cast<u32x4*>(p.dU + row * p.ld + n) = ou;
     }
 }
 
@@ -556,10 +588,17 @@ hipError_t launch_tile(const GatedParams& p, int tile, hipStream_t stream) {
     if (!p.direct) return launch_kernel<MODE, ACT, 128, 128, 2, 2, 1, PLANES>(p, stream);
     switch (tile) {
         //                                              BM   BN  WM WN ST
-        case GT_256x256: return launch_kernel<MODE, ACT, 256, 256, 2, 4, 2, PLANES>(p, stream);
+        case GT_160x256:
+            if constexpr (MODE != MODE_TN) return launch_kernel<MODE, ACT, 160, 256, 1, 4, 3, PLANES>(p, stream);
+            break;
+        case GT_256x128: return launch_kernel<MODE, ACT, 256, 128, 4, 2, 3, PLANES>(p, stream);
+        case GT_128x256: return launch_kernel<MODE, ACT, 128, 256, 2, 4, 3, PLANES>(p, stream);
         case GT_128x128: return launch_kernel<MODE, ACT, 128, 128, 2, 2, 2, PLANES>(p, stream);
-        default: return launch_kernel<MODE, ACT, 64, 128, 2, 2, 3, PLANES>(p, stream);
+        case GT_128x128_3: return launch_kernel<MODE, ACT, 128, 128, 2, 2, 3, PLANES>(p, stream);
+        case GT_64x128: return launch_kernel<MODE, ACT, 64, 128, 2, 2, 3, PLANES>(p, stream);
+        default: break;
     }
+    return launch_kernel<MODE, ACT, 256, 256, 2, 4, 2, PLANES>(p, stream);
 }
 
 // direct loads: rows at multiples of 16 bytes, a tile's rows within 32-bit offsets
@@ -575,6 +614,7 @@ hipError_t launch_gated(const GatedProblem& p, hipStream_t stream) {
     q.C0 = p.H;
     q.G = p.G;
     q.U = p.U;
+    q.kept = p.kept;
     q.M = (int)p.M;
     q.N = (int)p.N;
     q.K = (int)p.K;
@@ -619,12 +659,10 @@ hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t stream) {
     const int64_t chunks = (int64_t)p.M * (p.ld / 8);
     const int64_t blocks = (chunks + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-    if (p.act == BG_SILU)
-        hipLaunchKernelGGL(gate_grad_kernel<BG_SILU>, grid, dim3(256), 0, stream, p.dH, p.G, p.U, p.dG, p.dU, chunks, (int)p.N,
-                           (int)p.ld);
-    else
-        hipLaunchKernelGGL(gate_grad_kernel<BG_GELU_TANH>, grid, dim3(256), 0, stream, p.dH, p.G, p.U, p.dG, p.dU, chunks,
-                           (int)p.N, (int)p.ld);
+    const bool f32 = p.kept == BG_F32;
+    auto k = p.act == BG_SILU ? (f32 ? gate_grad_kernel<BG_SILU, true> : gate_grad_kernel<BG_SILU, false>)
+                              : (f32 ? gate_grad_kernel<BG_GELU_TANH, true> : gate_grad_kernel<BG_GELU_TANH, false>);
+    k<<<grid, dim3(256), 0, stream>>>(p, chunks);
     return hipGetLastError();
 }
 

@@ -576,16 +576,16 @@ typedef enum bg_activation { BG_SILU = 0, BG_GELU_TANH = 1 } bg_activation;
  * product on the FP32 sums.
  *
  *  A: [M, K], B0, B1: [N, K] BF16, read.  H: [M, N] BF16, written.
- *  G, U: both NULL, or [M, N] BF16, written: bf16(g) and bf16(u), which the
- *     gradient takes. One of them alone is BG_ERR_NULL.
+ *  G, U: both NULL, or [M, N] of kept_type (a bg_type), written: g and u, which
+ *     the gradient takes. One of them alone is BG_ERR_NULL.
  *  act: a bg_activation (BG_ERR_SHAPE otherwise).
  *  K % 8 != 0 takes a slower guarded load path. The summation order is fixed by
  *  the shape: repeated calls return identical bits. Outputs overlap neither an
  *  input nor each other (BG_ERR_ALIAS). A launch's grid holds ceil(M / 256) *
  *  ceil(N / 128) < 2^23 (BG_ERR_SHAPE otherwise).
  */
-bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, uint16_t* G, uint16_t* U,
-                          int act, uint32_t M, uint32_t N, uint32_t K, void* stream);
+bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, void* G, void* U,
+                          int kept_type, int act, uint32_t M, uint32_t N, uint32_t K, void* stream);
 
 /*
  * gemm_bf16_gated_backward: the gradients of gemm_bf16_gated for a gradient dH of
@@ -593,7 +593,11 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
  *   dG = bf16(dH * u * act'(g)), dU = bf16(dH * act(g)), on g and u as they were kept;
  *   dA = bf16(dG B0 + dU B1), dB0 = bf16(dG^T A), dB1 = bf16(dU^T A), FP32 sums.
  *
- *  dH, G, U: [M, N], A: [M, K], B0, B1: [N, K] BF16, read.
+ *  dH: [M, N], A: [M, K], B0, B1: [N, K] BF16, read.  G, U: [M, N] of kept_type, read.
+ *     The roundings of dG and dU are the only ones between FP32 sums with G and U
+ *     in FP32: a gradient is then about 1.4 times as far from the exact one (in
+ *     the mean) as its own rounding to BF16; kept in BF16, half the memory, 1.8
+ *     times.
  *  dA: [M, K] or NULL (not wanted; B0 and B1 are then not read).
  *  dB0, dB1: [N, K], or both NULL (A is then not read).
  *  workspace: device buffer of gemm_bf16_gated_backward_workspace(M, N, K) bytes,
@@ -604,8 +608,8 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
  *  gemm_bf16_nn and gemm_bf16_tn for the three products.
  */
 bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const uint16_t* B0, const uint16_t* B1,
-                                   const uint16_t* G, const uint16_t* U, uint16_t* dA, uint16_t* dB0, uint16_t* dB1, int act,
-                                   void* workspace, size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, void* stream);
+                                   const void* G, const void* U, int kept_type, uint16_t* dA, uint16_t* dB0, uint16_t* dB1,
+                                   int act, void* workspace, size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, void* stream);
 
 /* Bytes of workspace gemm_bf16_gated_backward needs on the current device, in
  * *bytes (a tile override changes it: query after setting one). */

@@ -8,7 +8,7 @@ from oracle import gated as og
 
 pytestmark = pytest.mark.gpu
 
-TILES = range(3)
+TILES = range(7)
 # one element, one row, less than a step, whole steps, odd everything, several
 # tiles of every size with ragged edges
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 130, 64), (64, 64, 64), (65, 127, 72), (128, 136, 128), (300, 200, 136),
@@ -21,10 +21,12 @@ def test_gated(m, n, k, act):
     a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.5 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
     h = bg.gemm_bf16_gated(a, b0, b1, act=act)
     check_gated(h, a, b0, b1, act, f"{m}x{n}x{k} {act}")
-    h2, g, u = bg.gemm_bf16_gated(a, b0, b1, act=act, save=True)
-    assert torch.equal(h, h2)
+    h2, g, u = bg.gemm_bf16_gated(a, b0, b1, act=act, save=torch.bfloat16)
+    h3, g32, u32 = bg.gemm_bf16_gated(a, b0, b1, act=act, save=True)
+    assert torch.equal(h, h2) and torch.equal(h, h3)
     check_product(g, a, b0.t(), "G")
     check_product(u, a, b1.t(), "U")
+    assert g32.dtype == torch.float32 and torch.equal(g32.bfloat16(), g) and torch.equal(u32.bfloat16(), u)
 
 
 @pytest.mark.parametrize("tile", TILES)
@@ -65,12 +67,13 @@ def test_split_reduction_is_exact_on_whole_numbers(m, n, k, tile, splits, force)
         assert torch.equal(bg.gemm_bf16_tn(a.t().contiguous(), b), want)
 
 
+@pytest.mark.parametrize("kept", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("m,n,k", SHAPES + [(1030, 72, 64), (40, 3000, 136)])
-def test_backward(m, n, k, act):
+def test_backward(m, n, k, act, kept):
     a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.5 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
     dh = normal((m, n), 0.01, 4)
-    _, g, u = bg.gemm_bf16_gated(a, b0, b1, act=act, save=True)
+    _, g, u = bg.gemm_bf16_gated(a, b0, b1, act=act, save=kept)
     grads = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u, act=act)
     check_backward(*grads, dh, a, b0, b1, g, u, act, f"{m}x{n}x{k} {act}")
     da, n0, n1 = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u, act=act, need_b=False)
