@@ -140,7 +140,7 @@ bg_status check_w4(const bg_w4* w, uint32_t N, uint32_t K, Operand (&ops)[3]) {
 
 bg_status gemv(const uint16_t* x, const bg_w4* w0, const bg_w4* w1, uint16_t* y, bool gated, int act, uint32_t R, uint32_t N,
                uint32_t K, void* stream) {
-    if (!dims_ok(R, N, K) || K % 32 != 0 || R > kMaxGemvRows || !act_ok(act) || !fits(R, K, 2) || !fits(N, K, 2) ||
+    if (!dims_ok(R, N, K) || K % 32 != 0 || K > kMaxGemvK || R > kMaxGemvRows || !act_ok(act) || !fits(R, K, 2) || !fits(N, K, 2) ||
         !fits(R, N, 2))
         return BG_ERR_SHAPE;
     // a launch holds fewer than 2^32 threads: 1024 for 16 columns and 16 rows at most

@@ -155,6 +155,7 @@ struct GemvProblem {
 // Pieces of 512 elements (a wave's) of a row of mxfp4_quantize, which numbers those of all rows in 32 bits.
 constexpr uint32_t mx_quant_pieces(uint32_t K) { return K / 512 + (K % 512 != 0); }
 constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 bytes stay within 32-bit offsets
+constexpr uint32_t kMaxGemvK = 1u << 20;      // block / group by one 32-bit multiplication
 constexpr uint32_t kMaxGemvRows = 1u << 16;   // sixteen rows of a grid's y
 constexpr uint32_t kMaxExperts = 1024;   // routing and grouped products
 constexpr uint32_t kMaxTopK = 16;

@@ -37,7 +37,9 @@ struct GemvParams {
     const uint16_t* x;
     W4Operand w[2];
     uint16_t* y;
-    int R, N, K, group;
+    int R, N, K, group, groups;     // groups: of a row
+    int act;
+    uint32_t per_group;   // int4: 2^32 over the group's 32-element blocks, rounded up: exact for K <= 2^20 (0 for one block)
 };
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -90,112 +92,175 @@ __device__ __forceinline__ bf16x8 nvfp4_values(uint32_t w, float scale) {
     return __builtin_bit_cast(bf16x8, u);
 }
 
-// What a lane holds of 128 elements of K of its weight row.
-struct Held {
-    u32x4 codes;
-    uint32_t scale;     // mxfp4: the byte; nvfp4: two bytes; int4: s in the upper half, z in the lower
-};
+// Four bytes p[at ..] of an array of size > 0 bytes on a 16-byte boundary, still
+// to be shifted down by `shift` bits. Those past its end are anything; no aligned
+// word is read that holds none of it.
+__device__ __forceinline__ uint32_t bytes_at(const uint8_t* p, int64_t at, int64_t size, uint32_t& shift) {
+    typedef uint32_t Word __attribute__((aligned(1)));
+    const int64_t from = min(at, (size + 3) / 4 * 4 - 4);
+    shift = 8 * (uint32_t)(at - from);
+    return *reinterpret_cast<const Word*>(p + from);
+}
 
-// GB: 32-element blocks of a 128-element load that certainly share a group
+// A workgroup is KW x NW waves: wave (kw, nw) takes NR times 16 weight rows (of
+// both matrices where gated) and every KW-th stretch of SPAN elements of K. x goes
+// through LDS, one chunk of KW stretches at a time for all waves, double buffered;
+// the codes and scales of the next stretch are in flight in registers while one is
+// multiplied.
+// RP: rows of x that LDS holds (R <= RP, or 16 at a time).
+// GB: 32-element blocks of a 128-element block that certainly share a group
 // (int4: 1, 2 or 4).
-template <int FORMAT, int GB, int WAVES, bool GATED, int ACT>
-__global__ void __launch_bounds__(WAVES * 64)
+constexpr int SPAN = 4 * BLOCK;
+
+template <int FORMAT, int GB, int RP, int KW, int NW, int NR, bool GATED>
+__global__ void __launch_bounds__(KW * NW * 64)
 gemv_w4_kernel(GemvParams p) {
-    constexpr int SETS = GATED ? 2 : 1, DEEP = GATED ? 2 : 4;
+    constexpr int MATS = GATED ? 2 : 1, SETS = NR * MATS;      // set s: matrix s % MATS, rows s / MATS
     constexpr bool INT4 = FORMAT == BG_W4_INT4, EXCHANGE = INT4 && GB < 4;
-    constexpr int PAD = 20;                     // floats between weight rows: 16 sums, aligned, over all banks
-    __shared__ __attribute__((aligned(16))) float sums[SETS][WAVES][16][PAD];
+    constexpr int NT = KW * NW * 64, ROWS = 16 * NR * NW;      // weight rows of the workgroup
+    constexpr int CHUNK = KW * SPAN, PITCH = CHUNK + 8;        // 16 rows of x: all banks
+    constexpr int XREGS = (RP * CHUNK / 8 + NT - 1) / NT;
+    constexpr int PAD = 20;                                    // floats between weight rows of the sums
+    constexpr int XBYTES = 2 * RP * PITCH * 2, SBYTES = SETS * KW * NW * 16 * PAD * 4;
+    // words that hold a block's scales: mxfp4 4 bytes, nvfp4 8, int4 one per group
+    constexpr int WORDS = FORMAT == BG_W4_MXFP4 ? 1 : FORMAT == BG_W4_NVFP4 ? 2 : 4 / GB;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[XBYTES > SBYTES ? XBYTES : SBYTES];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16, r0 = blockIdx.y * 16;
+    const int kw = wave % KW, nw = wave / KW;
+    const int n0 = blockIdx.x * ROWS + nw * (16 * NR), r0 = blockIdx.y * 16;
     const int part = lane >> 4;
-    const int64_t row = min(n0 + (lane & 15), p.N - 1);
-    const uint16_t* x = p.x + (int64_t)min(r0 + (lane & 15), p.R - 1) * p.K;
+    const int rows = min(p.R - r0, RP);
+    const bool zeros = INT4 && p.w[0].zeros != nullptr;
+    int row[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) row[i] = min(n0 + 16 * i + (lane & 15), p.N - 1);
 
-    const int blocks = (p.K + BLOCK - 1) / BLOCK;
-    const int per = (blocks + WAVES - 1) / WAVES;
-    const int first = min(wave * per, blocks), last = min(first + per, blocks);
+    const int spans = (p.K + SPAN - 1) / SPAN, chunks = (spans + KW - 1) / KW;
+
+    struct Stage {
+        u32x4 codes[SETS][4];
+        // of block `part` of the stretch, as loaded (nothing may wait for them
+        // before the next loads are issued): four bytes and a shift, or s and z
+        uint32_t scale[SETS][WORDS], more[SETS][WORDS];
+    };
+    auto load = [&](Stage& t, int chunk) {
+        const int k0 = min(chunk * KW + kw, spans - 1) * SPAN;
+#pragma unroll
+        for (int s = 0; s < SETS; ++s) {
+            const W4Operand& w = p.w[s % MATS];
+            const int64_t r = row[s / MATS];
+            const uint8_t* codes = w.codes + r * (p.K / 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + i * BLOCK + part * 32;
+                t.codes[s][i] = *reinterpret_cast<const u32x4*>(codes + (k < p.K ? k / 2 : 0));
+            }
+            const int k = k0 + part * BLOCK;
+            if constexpr (FORMAT == BG_W4_MXFP4) {
+                const int64_t per = p.K / 32;
+                t.scale[s][0] = bytes_at(w.scales, r * per + (k < p.K ? k / 32 : 0), p.N * per, t.more[s][0]);
+            } else if constexpr (FORMAT == BG_W4_NVFP4) {
+                const int64_t per = p.K / 16;
+                const int64_t from = r * per + (k < p.K ? k / 16 : 0);
+                t.scale[s][0] = bytes_at(w.scales, from, p.N * per, t.more[s][0]);
+                t.scale[s][WORDS - 1] = bytes_at(w.scales, from + 4, p.N * per, t.more[s][WORDS - 1]);
+            } else {
+                const int64_t per = p.groups;
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) {
+                    const int ki = k + i * (BLOCK / WORDS);
+                    const int64_t at = r * per + (ki < p.K ? (p.per_group ? (int)__umulhi((uint32_t)ki / 32, p.per_group) : ki / 32) : 0);
+                    t.scale[s][i] = reinterpret_cast<const uint16_t*>(w.scales)[at];
+                    t.more[s][i] = zeros ? w.zeros[at] : 8u;
+                }
+            }
+        }
+    };
+
+    // x: zeros past the end of K; int4 in the order of its codes
+    u32x4 xr[XREGS];
+    auto load_x = [&](int chunk) {
+#pragma unroll
+        for (int i = 0; i < XREGS; ++i) {
+            const int q = tid + i * NT, r = q / (CHUNK / 8), k = chunk * CHUNK + q % (CHUNK / 8) * 8;
+            xr[i] = *reinterpret_cast<const u32x4*>(p.x + (int64_t)(r0 + min(r, rows - 1)) * p.K + min(k, p.K - 8));
+        }
+    };
+    auto store_x = [&](int chunk) {
+        uint16_t* buf = reinterpret_cast<uint16_t*>(lds) + (chunk & 1) * (RP * PITCH);
+#pragma unroll
+        for (int i = 0; i < XREGS; ++i) {
+            const int q = tid + i * NT, r = q / (CHUNK / 8), c = q % (CHUNK / 8);
+            const u32x4 v = chunk * CHUNK + c * 8 < p.K ? xr[i] : u32x4{0u, 0u, 0u, 0u};
+            if (r < RP) *reinterpret_cast<u32x4*>(buf + r * PITCH + c * 8) = INT4 ? __builtin_bit_cast(u32x4, x_pairs(v)) : v;
+        }
+    };
 
     f32x4 acc[SETS] = {};
 
-    // past the end of K: codes and scales that are finite; x is zero there
-    auto load = [&](const W4Operand& w, int b) {
-        Held h;
-        const int k = b * BLOCK + part * 32;
-        const bool in = k < p.K;
-        const int kc = in ? k : 0;
-        h.codes = *reinterpret_cast<const u32x4*>(w.codes + row * (p.K / 2) + kc / 2);
-        if constexpr (FORMAT == BG_W4_MXFP4) {
-            const uint32_t s = w.scales[row * (p.K / 32) + kc / 32];
-            h.scale = in ? s : 127u;
-        } else if constexpr (FORMAT == BG_W4_NVFP4) {
-            const uint32_t s = *reinterpret_cast<const uint16_t*>(w.scales + row * (p.K / 16) + kc / 16);
-            h.scale = in ? s : 0u;
-        } else {
-            const int64_t at = row * (p.K / p.group) + kc / p.group;
-            const uint32_t s = reinterpret_cast<const uint16_t*>(w.scales)[at];
-            const uint32_t z = w.zeros != nullptr ? w.zeros[at] : 8u;
-            h.scale = in ? s << 16 | z : 0u;
-        }
-        return h;
-    };
-
-    for (int b0 = first; b0 < last; b0 += DEEP) {
-        Held held[DEEP][SETS];
+    auto multiply = [&](const Stage& t, int chunk) {
+        const int k0 = (chunk * KW + kw) * SPAN;
+        if (k0 >= p.K) return;
+        const uint16_t* buf = reinterpret_cast<const uint16_t*>(lds) + (chunk & 1) * (RP * PITCH) +
+                              min(lane & 15, RP - 1) * PITCH + kw * SPAN + (EXCHANGE ? 8 * part : 32 * part);
+        // every lane gets the scales of all four blocks
+        uint32_t scale[SETS][WORDS][4];
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d)
+        for (int s = 0; s < SETS; ++s)
 #pragma unroll
-            for (int s = 0; s < SETS; ++s) held[d][s] = load(p.w[s], min(b0 + d, last - 1));
+            for (int w = 0; w < WORDS; ++w) {
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d) {
-            const int b = b0 + d;
-            if (b >= last) break;
-            u32x4 xv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = b * BLOCK + (EXCHANGE ? 32 * i + 8 * part : 32 * part + 8 * i);
-                xv[i] = k < p.K ? *reinterpret_cast<const u32x4*>(x + k) : u32x4{0u, 0u, 0u, 0u};
+                for (int i = 0; i < 4; ++i)
+                    scale[s][w][i] = INT4 ? t.scale[s][w] << 16 | t.more[s][w] : t.scale[s][w] >> (t.more[s][w] & 31);
+                exchange(scale[s][w]);
             }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            bf16x8 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = *reinterpret_cast<const bf16x8*>(buf + b * BLOCK + (EXCHANGE ? 32 : 8) * i);
             if constexpr (!INT4) {
+                const bool in = k0 + b * BLOCK + part * 32 < p.K;
 #pragma unroll
                 for (int s = 0; s < SETS; ++s) {
-                    const Held& h = held[d][s];
-                    f32x2 e4m3 = {};
-                    if constexpr (FORMAT == BG_W4_NVFP4) e4m3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(h.scale, 1.0f, false);
+                    if constexpr (FORMAT == BG_W4_MXFP4) {
+                        const uint32_t e = in ? scale[s][0][b] >> (8 * part) & 255u : 127u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bf16x8 v = FORMAT == BG_W4_MXFP4
-                                             ? mxfp4_values(h.codes[i], __builtin_bit_cast(float, h.scale << 23))
-                                             : nvfp4_values(h.codes[i], i < 2 ? e4m3.x : e4m3.y);
-                        acc[s] = mfma16(__builtin_bit_cast(bf16x8, xv[i]), v, acc[s]);
+                        for (int i = 0; i < 4; ++i)
+                            acc[s] = mfma16(x[i], mxfp4_values(t.codes[s][b][i], __builtin_bit_cast(float, e << 23)), acc[s]);
+                    } else {
+                        const uint32_t e = in ? scale[s][part >> 1 ? WORDS - 1 : 0][b] >> (16 * (part & 1)) : 0u;
+                        const f32x2 f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(e, 1.0f, false);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[s] = mfma16(x[i], nvfp4_values(t.codes[s][b][i], i < 2 ? f.x : f.y), acc[s]);
                     }
                 }
             } else {
                 const u32x4 ones4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
                 const bf16x8 ones = __builtin_bit_cast(bf16x8, ones4);
-                uint32_t codes[SETS][4], scale[SETS][4];
+                uint32_t codes[SETS][4];
 #pragma unroll
                 for (int s = 0; s < SETS; ++s) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) codes[s][i] = held[d][s].codes[i], scale[s][i] = held[d][s].scale;
-                    if constexpr (EXCHANGE) {
-                        exchange(codes[s]);
-                        exchange(scale[s]);
-                    }
+                    for (int i = 0; i < 4; ++i) codes[s][i] = t.codes[s][b][i];
+                    if constexpr (EXCHANGE) exchange(codes[s]);
                 }
 #pragma unroll
                 for (int g = 0; g < 4; g += GB) {
                     f32x4 sum = {}, prod[SETS] = {};
 #pragma unroll
                     for (int i = g; i < g + GB; ++i) {
-                        const bf16x8 xs = x_pairs(xv[i]);
-                        sum = mfma16(xs, ones, sum);
+                        sum = mfma16(x[i], ones, sum);
 #pragma unroll
-                        for (int s = 0; s < SETS; ++s) prod[s] = mfma16(xs, int4_pairs(codes[s][i]), prod[s]);
+                        for (int s = 0; s < SETS; ++s) prod[s] = mfma16(x[i], int4_pairs(codes[s][i]), prod[s]);
                     }
 #pragma unroll
                     for (int s = 0; s < SETS; ++s) {
-                        const float by = bf16_hi(scale[s][g]), off = 16.0f + (float)(scale[s][g] & 0xFFFFu);
+                        const uint32_t h = scale[s][g / GB][b];
+                        const float by = bf16_hi(h), off = 16.0f + (float)(h & 0xFFFFu);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             acc[s][e] = __builtin_fmaf(by, __builtin_fmaf(-off, sum[e], prod[s][e]), acc[s][e]);
@@ -203,50 +268,114 @@ gemv_w4_kernel(GemvParams p) {
                 }
             }
         }
+    };
+
+    // Loads have no condition around them: the compiler counts what is in flight.
+    if (chunks > 0) {
+        Stage a, b;
+        load_x(0);
+        load(a, 0);
+        store_x(0);
+        lds_barrier();
+        auto turn = [&](const Stage& now, Stage& next, int c) {
+            load_x(c + 1);
+            load(next, c + 1);
+            multiply(now, c);
+            store_x(c + 1);
+            lds_barrier();
+        };
+        int c = 0;
+        for (; c + 2 < chunks; c += 2) {
+            turn(a, b, c);
+            turn(b, a, c + 1);
+        }
+        if (c + 1 < chunks) {
+            turn(a, b, c);
+            multiply(b, c + 1);
+        } else {
+            multiply(a, c);
+        }
+        lds_barrier();
     }
 
+    float* sums = reinterpret_cast<float*>(lds);
+    auto at = [&](int s, int w, int n, int r) { return sums + ((s * (KW * NW) + w) * 16 + n) * PAD + r; };
 #pragma unroll
-    for (int s = 0; s < SETS; ++s) *reinterpret_cast<f32x4*>(&sums[s][wave][lane & 15][4 * part]) = acc[s];
+    for (int s = 0; s < SETS; ++s) *reinterpret_cast<f32x4*>(at(s, wave, lane & 15, 4 * part)) = acc[s];
     __syncthreads();
-    const int n = tid & 15, r = tid >> 4;
-    if (tid < 256 && n0 + n < p.N && r0 + r < p.R) {
-        float v[SETS];
+    for (int q = tid; q < rows * ROWS; q += NT) {
+        const int n = q % ROWS, r = q / ROWS;      // weight row n: wave n / (16 NR) of N, its set n / 16 % NR
+        if (blockIdx.x * ROWS + n >= (unsigned)p.N) continue;
+        float v[MATS];
 #pragma unroll
-        for (int s = 0; s < SETS; ++s) {
-            v[s] = sums[s][0][n][r];
+        for (int m = 0; m < MATS; ++m) {
+            const int s = n / 16 % NR * MATS + m, w0 = n / (16 * NR) * KW;
+            v[m] = *at(s, w0, n & 15, r);
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w) v[s] += sums[s][w][n][r];
-            if constexpr (FORMAT == BG_W4_NVFP4) v[s] *= p.w[s].scale_2;
+            for (int w = 1; w < KW; ++w) v[m] += *at(s, w0 + w, n & 15, r);
+            if constexpr (FORMAT == BG_W4_NVFP4) v[m] *= p.w[m].scale_2;
         }
-        const float out = GATED ? gate<ACT>(v[0]) * v[SETS - 1] : v[0];
-        p.y[(int64_t)(r0 + r) * p.N + n0 + n] = (uint16_t)pack_bf16x2(out, 0.0f);
+        float out = v[0];
+        if constexpr (GATED) out = (p.act == BG_SILU ? gate<BG_SILU>(v[0]) : gate<BG_GELU_TANH>(v[0])) * v[1];
+        p.y[(int64_t)(r0 + r) * p.N + blockIdx.x * ROWS + n] = (uint16_t)pack_bf16x2(out, 0.0f);
     }
 }
 
-template <int FORMAT, int GB, bool GATED, int ACT>
-hipError_t launch(const GemvParams& p, hipStream_t stream) {
-    constexpr int WAVES = 8;
-    const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)((p.R + 15) / 16));
-    hipLaunchKernelGGL((gemv_w4_kernel<FORMAT, GB, WAVES, GATED, ACT>), grid, dim3(WAVES * 64), 0, stream, p);
+template <int FORMAT, int GB, int RP, int KW, int NW, int NR, bool GATED>
+hipError_t launch_kernel(const GemvParams& p, hipStream_t stream) {
+    constexpr int ROWS = 16 * NR * NW;
+    const dim3 grid((unsigned)((p.N + ROWS - 1) / ROWS), (unsigned)((p.R + 15) / 16));
+    hipLaunchKernelGGL((gemv_w4_kernel<FORMAT, GB, RP, KW, NW, NR, GATED>), grid, dim3(KW * NW * 64), 0, stream, p);
     return hipGetLastError();
 }
 
-template <bool GATED, int ACT>
+template <int FORMAT, int GB, bool GATED>
+hipError_t launch(const GemvParams& p, hipStream_t stream) {
+    int c = tune(BG_TUNE_TILE);
+    if (c < 0) c = 1;
+    if (p.R > 4) {
+        switch (c) {
+            case 0: return launch_kernel<FORMAT, GB, 16, 4, 2, 1, GATED>(p, stream);
+            case 1: return launch_kernel<FORMAT, GB, 16, 2, 2, 1, GATED>(p, stream);
+            case 2: return launch_kernel<FORMAT, GB, 16, 2, 4, 1, GATED>(p, stream);
+            case 3: return launch_kernel<FORMAT, GB, 16, 4, 2, 2, GATED>(p, stream);
+            default: return launch_kernel<FORMAT, GB, 16, 2, 2, 2, GATED>(p, stream);
+        }
+    }
+    if (p.R > 1) {
+        switch (c) {
+            case 0: return launch_kernel<FORMAT, GB, 4, 4, 1, 1, GATED>(p, stream);
+            case 1: return launch_kernel<FORMAT, GB, 4, 4, 2, 1, GATED>(p, stream);
+            case 2: return launch_kernel<FORMAT, GB, 4, 8, 1, 1, GATED>(p, stream);
+            case 3: return launch_kernel<FORMAT, GB, 4, 2, 1, 1, GATED>(p, stream);
+            default: return launch_kernel<FORMAT, GB, 4, 2, 2, 1, GATED>(p, stream);
+        }
+    }
+    switch (c) {
+        case 0: return launch_kernel<FORMAT, GB, 1, 4, 1, 1, GATED>(p, stream);
+        case 1: return launch_kernel<FORMAT, GB, 1, 4, 2, 1, GATED>(p, stream);
+        case 2: return launch_kernel<FORMAT, GB, 1, 8, 1, 1, GATED>(p, stream);
+        case 3: return launch_kernel<FORMAT, GB, 1, 2, 1, 1, GATED>(p, stream);
+        default: return launch_kernel<FORMAT, GB, 1, 2, 2, 1, GATED>(p, stream);
+    }
+}
+
+template <bool GATED>
 hipError_t launch_format(const GemvParams& p, int format, hipStream_t stream) {
-    if (format == BG_W4_MXFP4) return launch<BG_W4_MXFP4, 4, GATED, ACT>(p, stream);
-    if (format == BG_W4_NVFP4) return launch<BG_W4_NVFP4, 4, GATED, ACT>(p, stream);
-    if (p.group % 128 == 0) return launch<BG_W4_INT4, 4, GATED, ACT>(p, stream);
-    if (p.group % 64 == 0) return launch<BG_W4_INT4, 2, GATED, ACT>(p, stream);
-    return launch<BG_W4_INT4, 1, GATED, ACT>(p, stream);
+    if (format == BG_W4_MXFP4) return launch<BG_W4_MXFP4, 4, GATED>(p, stream);
+    if (format == BG_W4_NVFP4) return launch<BG_W4_NVFP4, 4, GATED>(p, stream);
+    if (p.group % 128 == 0) return launch<BG_W4_INT4, 4, GATED>(p, stream);
+    if (p.group % 64 == 0) return launch<BG_W4_INT4, 2, GATED>(p, stream);
+    return launch<BG_W4_INT4, 1, GATED>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_gemv_w4(const GemvProblem& q, hipStream_t stream) {
-    const GemvParams p{q.x, {q.w[0], q.w[1]}, q.y, (int)q.R, (int)q.N, (int)q.K, (int)q.group};
-    if (!q.gated) return launch_format<false, BG_SILU>(p, q.format, stream);
-    return q.act == BG_SILU ? launch_format<true, BG_SILU>(p, q.format, stream)
-                            : launch_format<true, BG_GELU_TANH>(p, q.format, stream);
+    const uint32_t blocks = q.group / 32;
+    const GemvParams p{q.x, {q.w[0], q.w[1]}, q.y, (int)q.R, (int)q.N, (int)q.K, (int)q.group, (int)(q.K / q.group), q.act,
+                       blocks > 1 ? (uint32_t)((((uint64_t)1 << 32) + blocks - 1) / blocks) : 0u};
+    return q.gated ? launch_format<true>(p, q.format, stream) : launch_format<false>(p, q.format, stream);
 }
 
 }  // namespace bg

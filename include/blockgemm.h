@@ -666,15 +666,17 @@ typedef struct bg_w4 {
 
 /*
  * gemv_w4: Y[r,n] = bf16( sum_k X[r,k] w[n,k] ) for few rows, BF16 activations and
- * weights in 4 bits. Weights enter exactly, sums are FP32 in a fixed order:
- * repeated calls return identical bits, and a row's bits do not depend on the
- * other rows.
+ * weights in 4 bits. Weights enter exactly, sums are FP32 in an order
+ * fixed by the shape: repeated calls return identical bits, whatever the other
+ * rows hold.
  *
  *  X: [R, K] BF16, read.  W: the weights [N, K].  Y: [R, N] BF16, written; must not
  *  overlap an input (BG_ERR_ALIAS).
  *  Made for up to 16 rows; more are taken 16 at a time, the weights read again
- *  for each (R <= 65536). K % 32 == 0 and a grid of ceil(N / 16) * ceil(R / 16) <
+ *  for each (R <= 65536). K % 32 == 0, K <= 2^20 and a grid of ceil(N / 16) * ceil(R / 16) <
  *  2^22 (BG_ERR_SHAPE otherwise). All pointers 16-byte aligned (BG_ERR_ALIGN).
+ *  MXFP4 and NVFP4 scales: the up to three bytes behind the array in its last
+ *  aligned four-byte word are read too (never another word), and not used.
  *  INT4: s (sum (16 + q) x - (16 + z) sum x) per group, so an infinity in a row of X
  *  makes that row of Y NaN.
  */
