@@ -897,33 +897,41 @@ class _W4(ctypes.Structure):
 
 
 def _w4(w: W4Weights, k: int, what: str):
-    """(struct, N, device tensors) of weights with K = k."""
-    kind = _W4_FORMATS.get(w.format)
+    """(struct, N) of weights with K = k."""
+    codes, scales, fmt, group, zeros, scale_2 = w
+    kind = _W4_FORMATS.get(fmt)
     if kind is None:
-        raise ValueError(f"{what}: format must be one of {', '.join(map(repr, _W4_FORMATS))}, got {w.format!r}")
-    own = _W4_GROUPS.get(w.format)
-    group = own if w.group is None else w.group
+        raise ValueError(f"{what}: format must be one of {', '.join(map(repr, _W4_FORMATS))}, got {fmt!r}")
+    own = _W4_GROUPS.get(fmt)
+    if group is None:
+        group = own
     if group is None or group <= 0 or (group != own if own else group % 32 != 0):
-        raise ValueError(f"{what}: group of {w.format} weights must be {own or 'a multiple of 32'}, got {w.group}")
+        raise ValueError(f"{what}: group of {fmt} weights must be {own or 'a multiple of 32'}, got {w.group}")
     _blocks32(k)
     if k % group != 0:
         raise ValueError(f"{what}: K = {k} must be a multiple of the group, {group}")
-    n, _ = _dims(_bytes(w.codes, f"{what} codes"), 2, f"{what} codes")
-    _shape(w.codes, (n, k // 2), f"{what} codes")
-    scales = _bits16(w.scales, f"{what} scales") if own is None else _bytes(w.scales, f"{what} scales")
-    _shape(scales, (n, k // group), f"{what} scales")
-    if w.zeros is not None:
+    shape = _dims(_bytes(codes, what), 2, what)
+    n = shape[0]
+    if shape[1] != k // 2:
+        raise ValueError(f"{what}: codes must have shape {(n, k // 2)}, got {tuple(shape)}")
+    if own is None:
+        _bits16(scales, what)
+    else:
+        _bytes(scales, what)
+    _shape(scales, (n, k // group), what)
+    if zeros is not None:
         if own is not None:
-            raise ValueError(f"{what}: {w.format} weights have no zeros")
-        _shape(_bytes(w.zeros, f"{what} zeros"), (n, k // group), f"{what} zeros")
-    return _W4(_ptr(w.codes), _ptr(scales), _ptr(w.zeros), kind, group, w.scale_2), n, (w.codes, scales, w.zeros)
+            raise ValueError(f"{what}: {fmt} weights have no zeros")
+        _shape(_bytes(zeros, what), (n, k // group), what)
+    _on_device(codes, scales, zeros)
+    return _W4(_ptr(codes), _ptr(scales), _ptr(zeros), kind, group, scale_2), n
 
 
 def gemv_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, stream=None):
     """Y[R,N] = bf16(x[R,K] @ deq(W)^T) for few rows of bfloat16 activations (16 at a time)."""
     r, k = _dims(_bits16(x, "x"), 2, "x")
-    held, n, tensors = _w4(w, k, "W")
-    _on_device(x, *tensors, out)
+    held, n = _w4(w, k, "W")
+    _on_device(x, out)
     out = _out(out, (r, n), x, stream)
     _check(lib.gemv_w4(_ptr(x), ctypes.byref(held), _ptr(out), r, n, k, _stream(stream)), "gemv_w4")
     return out
@@ -934,11 +942,11 @@ def gemv_w4_gated(x: torch.Tensor, w0: W4Weights, w1: W4Weights, act: str = "sil
     """H[R,N] = bf16(act(x @ deq(W0)^T) * (x @ deq(W1)^T)) for few rows; both weights of one format and group."""
     kind = _activation(act)
     r, k = _dims(_bits16(x, "x"), 2, "x")
-    held0, n, t0 = _w4(w0, k, "W0")
-    held1, n1, t1 = _w4(w1, k, "W1")
+    held0, n = _w4(w0, k, "W0")
+    held1, n1 = _w4(w1, k, "W1")
     if n1 != n or held1.format != held0.format or held1.group != held0.group or (w0.zeros is None) != (w1.zeros is None):
         raise ValueError("W0 and W1 must have the same shape, format and group, both or neither zeros")
-    _on_device(x, *t0, *t1, out)
+    _on_device(x, out)
     out = _out(out, (r, n), x, stream)
     _check(lib.gemv_w4_gated(_ptr(x), ctypes.byref(held0), ctypes.byref(held1), _ptr(out), kind, r, n, k,
                              _stream(stream)), "gemv_w4_gated")

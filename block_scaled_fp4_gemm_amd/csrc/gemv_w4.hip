@@ -262,7 +262,7 @@ gemv_w4_kernel(GemvParams p) {
                         const uint32_t h = scale[s][g / GB][b];
                         const float by = bf16_hi(h), off = 16.0f + (float)(h & 0xFFFFu);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < (RP == 1 ? 1 : 4); ++e)      // row 0 is element 0
                             acc[s][e] = __builtin_fmaf(by, __builtin_fmaf(-off, sum[e], prod[s][e]), acc[s][e]);
                     }
                 }
@@ -329,44 +329,51 @@ hipError_t launch_kernel(const GemvParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Waves of a workgroup (KW x NW) by the 16-row groups of weights against the
+// compute units, the stretches of K, and the rows of x in LDS. Measured us:
+//  up to one group per unit, 8 x 1 where K has six stretches or more and 16 rows
+//  of x are not held (their chunk would not fit), else 4 x 1. One row, MXFP4:
+//  2048 x 11008 6.3 with 8 x 1, 6.8 with 4 x 1, 8.9 with 4 x 2; 512 x 2048 3.7, 3.1,
+//  3.6. 16 rows: 4096 x 7168 4 x 1 9.3, 4 x 2 10.2, 2 x 2 9.9.
+//  Up to two, 8 x 1 for up to four rows (7168 x 16384, one row, int4: 19.3; 4 x 1
+//  20.6, 4 x 2 19.7), 4 x 2 above (8 rows MXFP4 18.5, 4 x 1 21.8, 2 x 2 19.0; 16 rows
+//  21.9, 29.2, 22.6): two groups of weight rows then share x.
+//  More: 4 x 1 up to four rows (11008 x 2048, one row: 5.3; 8 x 1 7.3, 2 x 2 5.7), 2 x 2
+//  above (12287 x 2080, 8 rows: 6.8; 4 x 1 8.5, 4 x 2 7.7; 32000 x 2048, 16 rows: 13.0;
+//  4 x 1 25.1, 4 x 2 16.0).
+//  Gated, twice the weights in flight: 8 x 1 up to one group per unit (4096 x 11008,
+//  one row int4: 15.8; 4 x 1 17.7), and 4 x 1 up to eight rows past it (11008 x 4096, 8
+//  rows int4: 19.5; 2 x 2 22.1, 8 x 1 22.8).
+template <int FORMAT, int GB, int RP, bool GATED>
+hipError_t launch_rows(const GemvParams& p, uint32_t cus, hipStream_t stream) {
+    const uint32_t groups = ((uint32_t)p.N + 15) / 16, spans = ((uint32_t)p.K + SPAN - 1) / SPAN;
+    if constexpr (RP < 16) {
+        if (spans >= 6 && groups <= (RP <= 4 && !GATED ? 2 : 1) * cus)
+            return launch_kernel<FORMAT, GB, RP, 8, 1, 1, GATED>(p, stream);
+    }
+    if (groups <= cus || RP <= 4 || (GATED && RP <= 8)) return launch_kernel<FORMAT, GB, RP, 4, 1, 1, GATED>(p, stream);
+    if constexpr (RP > 4 && !(GATED && RP <= 8)) {
+        if (groups <= 2 * cus) return launch_kernel<FORMAT, GB, RP, 4, 2, 1, GATED>(p, stream);
+        return launch_kernel<FORMAT, GB, RP, 2, 2, 1, GATED>(p, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
 template <int FORMAT, int GB, bool GATED>
-hipError_t launch(const GemvParams& p, hipStream_t stream) {
-    int c = tune(BG_TUNE_TILE);
-    if (c < 0) c = 1;
-    if (p.R > 4) {
-        switch (c) {
-            case 0: return launch_kernel<FORMAT, GB, 16, 4, 2, 1, GATED>(p, stream);
-            case 1: return launch_kernel<FORMAT, GB, 16, 2, 2, 1, GATED>(p, stream);
-            case 2: return launch_kernel<FORMAT, GB, 16, 2, 4, 1, GATED>(p, stream);
-            case 3: return launch_kernel<FORMAT, GB, 16, 4, 2, 2, GATED>(p, stream);
-            default: return launch_kernel<FORMAT, GB, 16, 2, 2, 2, GATED>(p, stream);
-        }
-    }
-    if (p.R > 1) {
-        switch (c) {
-            case 0: return launch_kernel<FORMAT, GB, 4, 4, 1, 1, GATED>(p, stream);
-            case 1: return launch_kernel<FORMAT, GB, 4, 4, 2, 1, GATED>(p, stream);
-            case 2: return launch_kernel<FORMAT, GB, 4, 8, 1, 1, GATED>(p, stream);
-            case 3: return launch_kernel<FORMAT, GB, 4, 2, 1, 1, GATED>(p, stream);
-            default: return launch_kernel<FORMAT, GB, 4, 2, 2, 1, GATED>(p, stream);
-        }
-    }
-    switch (c) {
-        case 0: return launch_kernel<FORMAT, GB, 1, 4, 1, 1, GATED>(p, stream);
-        case 1: return launch_kernel<FORMAT, GB, 1, 4, 2, 1, GATED>(p, stream);
-        case 2: return launch_kernel<FORMAT, GB, 1, 8, 1, 1, GATED>(p, stream);
-        case 3: return launch_kernel<FORMAT, GB, 1, 2, 1, 1, GATED>(p, stream);
-        default: return launch_kernel<FORMAT, GB, 1, 2, 2, 1, GATED>(p, stream);
-    }
+hipError_t launch(const GemvParams& p, uint32_t cus, hipStream_t stream) {
+    if (p.R == 1) return launch_rows<FORMAT, GB, 1, GATED>(p, cus, stream);
+    if (p.R <= 4) return launch_rows<FORMAT, GB, 4, GATED>(p, cus, stream);
+    if (p.R <= 8) return launch_rows<FORMAT, GB, 8, GATED>(p, cus, stream);
+    return launch_rows<FORMAT, GB, 16, GATED>(p, cus, stream);
 }
 
 template <bool GATED>
-hipError_t launch_format(const GemvParams& p, int format, hipStream_t stream) {
-    if (format == BG_W4_MXFP4) return launch<BG_W4_MXFP4, 4, GATED>(p, stream);
-    if (format == BG_W4_NVFP4) return launch<BG_W4_NVFP4, 4, GATED>(p, stream);
-    if (p.group % 128 == 0) return launch<BG_W4_INT4, 4, GATED>(p, stream);
-    if (p.group % 64 == 0) return launch<BG_W4_INT4, 2, GATED>(p, stream);
-    return launch<BG_W4_INT4, 1, GATED>(p, stream);
+hipError_t launch_format(const GemvParams& p, int format, uint32_t cus, hipStream_t stream) {
+    if (format == BG_W4_MXFP4) return launch<BG_W4_MXFP4, 4, GATED>(p, cus, stream);
+    if (format == BG_W4_NVFP4) return launch<BG_W4_NVFP4, 4, GATED>(p, cus, stream);
+    if (p.group % 128 == 0) return launch<BG_W4_INT4, 4, GATED>(p, cus, stream);
+    if (p.group % 64 == 0) return launch<BG_W4_INT4, 2, GATED>(p, cus, stream);
+    return launch<BG_W4_INT4, 1, GATED>(p, cus, stream);
 }
 
 }  // namespace
@@ -375,7 +382,7 @@ hipError_t launch_gemv_w4(const GemvProblem& q, hipStream_t stream) {
     const uint32_t blocks = q.group / 32;
     const GemvParams p{q.x, {q.w[0], q.w[1]}, q.y, (int)q.R, (int)q.N, (int)q.K, (int)q.group, (int)(q.K / q.group), q.act,
                        blocks > 1 ? (uint32_t)((((uint64_t)1 << 32) + blocks - 1) / blocks) : 0u};
-    return q.gated ? launch_format<true>(p, q.format, stream) : launch_format<false>(p, q.format, stream);
+    return q.gated ? launch_format<true>(p, q.format, q.cus, stream) : launch_format<false>(p, q.format, q.cus, stream);
 }
 
 }  // namespace bg
