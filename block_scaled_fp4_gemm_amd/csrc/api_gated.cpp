@@ -48,9 +48,12 @@ bg_status check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
 
 uint32_t pitch8(uint32_t n) { return (n + 7) / 8 * 8; }
 
-// An nn (C [M, N] of K terms, parts of them) or tn (parts outputs) product.
-GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t parts, uint32_t cus) {
-    return plan_of(false, M, N, tn ? K / 64 : K / 64 * parts, tn ? parts : 1, cus, tune(BG_TUNE_TILE));
+// An nn (C [M, N] of K terms, parts of them) or tn (parts outputs) product, A's
+// rows lda elements apart.
+GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t lda, uint32_t parts, uint32_t cus) {
+    const bool direct = gated_direct(lda) && gated_direct(N);
+    const uint32_t steps = direct ? K / 64 : K / 64 + (K % 64 != 0);
+    return plan_of(false, tn, direct, M, N, tn ? steps : steps * parts, tn ? parts : 1, cus, tune(BG_TUNE_TILE));
 }
 uint64_t planes_bytes(const GatedPlan& p, uint32_t M, uint32_t N, uint32_t outputs) {
     return p.splits > 1 ? (uint64_t)p.splits * outputs * M * N * 4 : 0;
@@ -67,7 +70,7 @@ bg_status transposed_workspace(bool tn, uint32_t M, uint32_t N, uint32_t K, size
     uint32_t cus = 0;
     const bg_status s = check_device(&cus);
     if (s != BG_OK) return s;
-    *bytes = M == 0 || N == 0 ? 0 : (size_t)planes_bytes(transposed_plan(tn, M, N, K, 1, cus), M, N, 1);
+    *bytes = M == 0 || N == 0 ? 0 : (size_t)planes_bytes(transposed_plan(tn, M, N, K, tn ? M : K, 1, cus), M, N, 1);
     return BG_OK;
 }
 
@@ -81,7 +84,7 @@ bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C,
     if (s != BG_OK) return s;
     uint32_t cus = 0;
     if ((s = check_device(&cus)) != BG_OK) return s;
-    const GatedPlan plan = transposed_plan(tn, M, N, K, 1, cus);
+    const GatedPlan plan = transposed_plan(tn, M, N, K, tn ? M : K, 1, cus);
     const uint64_t need = planes_bytes(plan, M, N, 1);
     if (need != 0) {
         if (ws == nullptr || ws_bytes < need) return BG_ERR_WORKSPACE;
@@ -105,8 +108,8 @@ struct GradPlan {
 };
 GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
     GradPlan g;
-    g.nn = transposed_plan(false, M, K, N, 2, cus);
-    g.tn = transposed_plan(true, N, K, M, 2, cus);
+    g.nn = transposed_plan(false, M, K, N, pitch8(N), 2, cus);
+    g.tn = transposed_plan(true, N, K, M, pitch8(N), 2, cus);
     g.half = (uint64_t)M * pitch8(N) * 2;
     const uint64_t a = planes_bytes(g.nn, M, K, 1), b = planes_bytes(g.tn, N, K, 2);
     g.bytes = 2 * g.half + (a > b ? a : b);
@@ -190,7 +193,7 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
     if (s != BG_OK) return s;
     uint32_t cus = 0;
     if ((s = check_device(&cus)) != BG_OK) return s;
-    const GatedPlan plan = plan_of(true, M, N, K / 64, 1, cus, tune(BG_TUNE_TILE));
+    const GatedPlan plan = plan_of(true, false, gated_direct(K), M, N, K / 64, 1, cus, tune(BG_TUNE_TILE));
     return launched(launch_gated(GatedProblem{A, B0, B1, H, G, U, kept_type, M, N, K, act, plan.tile}, (hipStream_t)stream));
 }
 

@@ -7,15 +7,32 @@
 
 namespace bg {
 
-enum GatedTile : int { GT_256x256, GT_160x256, GT_256x128, GT_128x256, GT_128x128, GT_128x128_3, GT_64x128, GT_TILES };
-struct GatedTileSize {
+// us: per tile; per step of 64 with few tiles on the chip, with one on every
+// compute unit, and, where two fit a unit's LDS, the tile and the step of a pair
+// (0: one workgroup fills it). Medians over the three products, 32 to 1024 tiles
+// and K 512 to 6144; the sum is within 10% of most of them.
+struct GatedTileInfo {
     int bm, bn, threads;
+    double fixed, few, full, pair_fixed, pair;
 };
-constexpr GatedTileSize kGatedTiles[GT_TILES] = {{256, 256, 512}, {160, 256, 256}, {256, 128, 512}, {128, 256, 512},
-                                                     {128, 128, 256}, {128, 128, 256}, {64, 128, 256}};
+enum GatedTile : int { GT_256x256, GT_160x256, GT_256x128, GT_128x128, GT_128x128_DEEP, GT_64x128, GT_TILES };
+constexpr GatedTileInfo kGatedTiles[GT_TILES] = {{256, 256, 512, 9.0, 1.25, 1.72, 0, 0},
+                                                 {160, 256, 256, 7.5, 0.80, 1.20, 0, 0},
+                                                 {256, 128, 512, 5.7, 0.68, 1.04, 0, 0},
+                                                 {128, 128, 256, 4.0, 0.70, 0.78, 5.0, 1.02},
+                                                 {128, 128, 512, 4.8, 0.41, 0.58, 0, 0},
+                                                 {64, 128, 256, 4.4, 0.48, 0.52, 4.6, 0.69}};
+
+// Rows that do not start at multiples of 16 bytes: 128 x 128 tiles, every step
+// loaded through registers with checks.
+constexpr GatedTileInfo kGuarded = {128, 128, 256, 5.0, 2.4, 2.6, 6.0, 3.6};
 
 // Output columns of a tile of bn operand rows: a gated tile holds both products.
 constexpr int tile_columns(int bn, bool gated) { return gated ? bn / 2 : bn; }
+
+// Direct loads: rows `ld` elements apart start at multiples of 16 bytes, and a
+// tile's rows lie within 32-bit offsets.
+inline bool gated_direct(uint32_t ld) { return ld % 8 == 0 && (uint64_t)ld * 512 < ((uint64_t)1 << 31); }
 
 struct GatedPlan {
     int tile, splits;
@@ -24,7 +41,7 @@ struct GatedPlan {
 inline uint64_t gated_ceil(uint64_t n, uint64_t by) { return (n + by - 1) / by; }
 
 inline uint64_t gated_tiles(int tile, bool gated, uint32_t M, uint32_t N, uint32_t outputs) {
-    const GatedTileSize& t = kGatedTiles[tile];
+    const GatedTileInfo& t = kGatedTiles[tile];
     return gated_ceil(M, t.bm) * gated_ceil(N, tile_columns(t.bn, gated)) * outputs;
 }
 
@@ -33,20 +50,58 @@ inline bool gated_launches(const GatedPlan& p, bool gated, uint32_t M, uint32_t 
     return gated_tiles(p.tile, gated, M, N, outputs) * p.splits * kGatedTiles[p.tile].threads < ((uint64_t)1 << 32);
 }
 
-inline GatedPlan plan_of(bool gated, uint32_t M, uint32_t N, uint32_t steps, uint32_t outputs, uint32_t cus, int forced) {
-    GatedPlan p{GT_256x256, 1};
+// n tiles of `steps` steps in rounds over the compute units.
+inline double gated_us(const GatedTileInfo& t, uint64_t n, double steps, uint32_t cus) {
+    const uint64_t slots = t.pair > 0 ? 2 * (uint64_t)cus : cus;
+    const double round = t.pair > 0 ? t.pair_fixed + steps * t.pair : t.fixed + steps * t.full;
+    const uint64_t rest = n % slots;
+    double us = (double)(n / slots) * round;
+    if (rest > cus)
+        us += round;
+    else if (rest != 0)
+        us += t.fixed + steps * (t.few + (t.full - t.few) * (double)rest / cus);
+    return us;
+}
+
+// The planes of a split reduction: written by the product and read by their sum
+// (at about 4 bytes a ps), and the second launch.
+inline double planes_us(uint32_t M, uint32_t N, uint32_t outputs, int splits) {
+    return splits == 1 ? 0.0 : 4.0 + (double)M * N * outputs * splits * 8e-6 / 4.0;
+}
+
+constexpr int kMaxSplits = 16;
+
+// The tile, and the number of parts of the reduction (products without a
+// workspace: one), whose time by the table is least. Without direct loads there is
+// one tile (kGuarded). `forced` >= 0: tile forced % 16 and forced / 16 parts.
+inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t N, uint32_t steps, uint32_t outputs, uint32_t cus,
+                         int forced) {
+    const int most = steps < 2 ? 1 : steps < (uint32_t)kMaxSplits ? (int)steps : kMaxSplits;
+    auto ok = [&](const GatedPlan& p) {
+        return !(tn && p.tile == GT_160x256) && (p.tile == GT_256x256 || gated_launches(p, gated, M, N, outputs));
+    };
     if (forced >= 0) {
-        p.tile = forced % 16 < GT_TILES ? forced % 16 : GT_256x256;
-        if (!gated && forced >= 16) p.splits = forced / 16;
-    } else {
-        if (gated_tiles(GT_256x256, gated, M, N, outputs) < cus) p.tile = M <= 64 ? GT_64x128 : GT_128x128;
-        if (!gated) {
-            const uint64_t n = gated_tiles(p.tile, gated, M, N, outputs);
-            while (n * p.splits * 2 <= 2 * cus && p.splits < 16 && steps / (p.splits * 2) >= 4) p.splits *= 2;
+        GatedPlan p{forced % 16 < GT_TILES ? forced % 16 : GT_256x256, 1};
+        if (!gated && forced >= 16) p.splits = forced / 16 < most ? forced / 16 : most;
+        if (!ok(p)) p = GatedPlan{GT_256x256, 1};
+        return p;
+    }
+    GatedPlan best{GT_256x256, 1};
+    double least = -1;
+    for (int tile = direct ? 0 : GT_128x128; tile < (direct ? (int)GT_TILES : GT_128x128 + 1); ++tile) {
+        const GatedTileInfo& info = direct ? kGatedTiles[tile] : kGuarded;
+        const uint64_t n = gated_tiles(tile, gated, M, N, outputs);
+        for (int splits = 1; splits <= (gated ? 1 : most); ++splits) {
+            // parts of less than four steps, or parts that no unit waits for, gain nothing
+            if (splits > 1 && (steps / splits < (direct ? 4 : 1) || n * (splits - 1) >= 2 * (uint64_t)cus)) break;
+            const GatedPlan p{tile, splits};
+            if (!ok(p)) continue;
+            const double us = gated_us(info, n * splits, (double)gated_ceil(steps ? steps : 1, splits), cus) +
+                              planes_us(M, N, outputs, splits);
+            if (least < 0 || us < least) best = p, least = us;
         }
     }
-    if (p.splits > (int)steps) p.splits = steps > 1 ? (int)steps : 1;
-    return p;
+    return best;
 }
 
 }  // namespace bg

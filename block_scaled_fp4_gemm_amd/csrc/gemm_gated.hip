@@ -286,6 +286,34 @@ __device__ __forceinline__ void store_tile(OUT* C, int64_t ldc, int M, int N, in
     }
 }
 
+// FP32 results straight from the accumulators: a lane's four columns are 16 bytes,
+// two lanes' 32 consecutive bytes of a row, and the next stores complete the lines.
+template <int BM, int BNO, int WM, int WN, int FM, int JN, class Value>
+__device__ __forceinline__ void store_direct(float* C, int64_t ldc, int M, int N, int m0, int n0, int wm, int wn, int lane,
+                                             Value&& value) {
+    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int m = m0 + wm * (BM / WM) + i * 32 + (lane & 31);
+        if (m >= M) continue;
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int n = n0 + wn * (BNO / WN) + j * 32 + g * 8 + (lane >> 5) * 4;
+                float* dst = C + (int64_t)m * ldc + n;
+                const f32x4 v = {value(i, j, 4 * g), value(i, j, 4 * g + 1), value(i, j, 4 * g + 2), value(i, j, 4 * g + 3)};
+                if (n + 4 <= N) {
+                    *reinterpret_cast<f32x4_any*>(dst) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < N) dst[e] = v[e];
+                }
+            }
+    }
+}
+
 // STAGES == 1: every step guarded, for rows that do not start at multiples of 16 bytes.
 template <int MODE, int ACT, int BM, int BN, int WM, int WN, int STAGES, bool PLANES>
 __global__ void __launch_bounds__(WM * WN * 64)
@@ -460,8 +488,8 @@ gated_kernel(GatedParams p) {
             auto g = [&](int i, int j, int e) { return acc[i][2 * j][e]; };
             auto u = [&](int i, int j, int e) { return acc[i][2 * j + 1][e]; };
             if (p.kept == BG_F32) {
-                out(static_cast<float*>(p.G), g);
-                out(static_cast<float*>(p.U), u);
+                store_direct<BM, BNO, WM, WN, FM, FN / 2>(static_cast<float*>(p.G), p.N, p.M, p.N, m0, n0, wm, wn, elane, g);
+                store_direct<BM, BNO, WM, WN, FM, FN / 2>(static_cast<float*>(p.U), p.N, p.M, p.N, m0, n0, wm, wn, elane, u);
             } else {
                 out(static_cast<uint16_t*>(p.G), g);
                 out(static_cast<uint16_t*>(p.U), u);
@@ -592,17 +620,13 @@ hipError_t launch_tile(const GatedParams& p, int tile, hipStream_t stream) {
             if constexpr (MODE != MODE_TN) return launch_kernel<MODE, ACT, 160, 256, 1, 4, 3, PLANES>(p, stream);
             break;
         case GT_256x128: return launch_kernel<MODE, ACT, 256, 128, 4, 2, 3, PLANES>(p, stream);
-        case GT_128x256: return launch_kernel<MODE, ACT, 128, 256, 2, 4, 3, PLANES>(p, stream);
         case GT_128x128: return launch_kernel<MODE, ACT, 128, 128, 2, 2, 2, PLANES>(p, stream);
-        case GT_128x128_3: return launch_kernel<MODE, ACT, 128, 128, 2, 2, 3, PLANES>(p, stream);
+        case GT_128x128_DEEP: return launch_kernel<MODE, ACT, 128, 128, 4, 2, 4, PLANES>(p, stream);
         case GT_64x128: return launch_kernel<MODE, ACT, 64, 128, 2, 2, 3, PLANES>(p, stream);
         default: break;
     }
     return launch_kernel<MODE, ACT, 256, 256, 2, 4, 2, PLANES>(p, stream);
 }
-
-// direct loads: rows at multiples of 16 bytes, a tile's rows within 32-bit offsets
-bool direct_ok(uint32_t ld) { return ld % 8 == 0 && (int64_t)ld * 512 < (int64_t(1) << 31); }
 
 }  // namespace
 
@@ -620,7 +644,7 @@ hipError_t launch_gated(const GatedProblem& p, hipStream_t stream) {
     q.K = (int)p.K;
     q.lda = q.ldb = (int)p.K;
     q.parts = q.splits = 1;
-    q.direct = direct_ok(p.K);
+    q.direct = gated_direct(p.K);
     return p.act == BG_SILU ? launch_tile<MODE_GATED, BG_SILU, false>(q, p.tile, stream)
                             : launch_tile<MODE_GATED, BG_GELU_TANH, false>(q, p.tile, stream);
 }
@@ -638,7 +662,7 @@ hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
     q.ldb = (int)p.N;
     q.parts = (int)p.parts;
     q.splits = (int)p.splits;
-    q.direct = direct_ok(p.lda) && direct_ok(p.N);
+    q.direct = gated_direct(p.lda) && gated_direct(p.N);
     if (p.splits == 1) {
         q.C0 = p.C0;
         q.C1 = p.C1;

@@ -8,7 +8,7 @@ from oracle import gated as og
 
 pytestmark = pytest.mark.gpu
 
-TILES = range(7)
+TILES = range(6)
 # one element, one row, less than a step, whole steps, odd everything, several
 # tiles of every size with ragged edges
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 130, 64), (64, 64, 64), (65, 127, 72), (128, 136, 128), (300, 200, 136),
