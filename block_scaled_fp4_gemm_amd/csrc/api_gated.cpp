@@ -92,7 +92,7 @@ bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C,
         if ((s = check_operands(with, planes)) != BG_OK) return s;
     }
     return launched(launch_transposed(TransposedProblem{tn, A, nullptr, B, nullptr, C, nullptr, static_cast<float*>(ws), M, N, K,
-                                                        tn ? M : K, 1, plan.tile, plan.splits},
+                                                        tn ? M : K, 1, plan.tile, plan.splits, 0, 1},
                                       (hipStream_t)stream));
 }
 
@@ -101,17 +101,22 @@ bool gated_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
            fits(M, N, 4) && gated_launches(GatedPlan{GT_256x256, 1}, true, M, N, 1);
 }
 
-// The gradient's workspace: dG and dU, then the larger of the two products' planes.
+// The gradient's workspace: dG and dU, each followed by its low half where M is
+// small, then the larger of the two products' planes.
 struct GradPlan {
     GatedPlan nn, tn;
-    uint64_t half, bytes;    // of dG; of all
+    uint32_t stacked;        // 2 with low halves: dA's product runs over both as 2 M rows
+    uint64_t half, bytes;    // of dG (with its low half); of all
 };
 GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
     GradPlan g;
-    g.nn = transposed_plan(false, M, K, N, pitch8(N), 2, cus);
+    g.stacked = M <= kFineRows ? 2 : 1;
+    g.nn = transposed_plan(false, M * g.stacked, K, N, pitch8(N), 2, cus);
     g.tn = transposed_plan(true, N, K, M, pitch8(N), 2, cus);
-    g.half = (uint64_t)M * pitch8(N) * 2;
-    const uint64_t a = planes_bytes(g.nn, M, K, 1), b = planes_bytes(g.tn, N, K, 2);
+    g.half = (uint64_t)M * pitch8(N) * 2 * g.stacked;
+    const uint64_t rows = (uint64_t)M * g.stacked;
+    const uint64_t a = g.nn.splits > 1 || g.stacked > 1 ? (uint64_t)g.nn.splits * rows * K * 4 : 0;
+    const uint64_t b = planes_bytes(g.tn, N, K, 2);
     g.bytes = 2 * g.half + (a > b ? a : b);
     return g;
 }
@@ -248,17 +253,18 @@ bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const 
     uint16_t* dU = dG + plan.half / 2;
     float* planes = reinterpret_cast<float*>(dU + plan.half / 2);
     const uint32_t ld = pitch8(N);
+    const int64_t low = plan.stacked > 1 ? (int64_t)M * ld : 0;
     const bool want_a = dA != nullptr && M != 0 && K != 0, want_b = dB0 != nullptr && N != 0 && K != 0;
     if (!want_a && !want_b) return BG_OK;
     hipError_t e = hipSuccess;
-    if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, kept_type, dG, dU, M, N, ld, act}, st);
+    if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, kept_type, dG, dU, M, N, ld, act, low}, st);
     if (e == hipSuccess && want_a)
-        e = launch_transposed(TransposedProblem{false, dG, dU, B0, B1, dA, nullptr, planes, M, K, N, ld, 2, plan.nn.tile,
-                                                plan.nn.splits},
+        e = launch_transposed(TransposedProblem{false, dG, dU, B0, B1, dA, nullptr, planes, M * plan.stacked, K, N, ld, 2,
+                                                plan.nn.tile, plan.nn.splits, 0, plan.stacked},
                               st);
     if (e == hipSuccess && want_b)
         e = launch_transposed(TransposedProblem{true, dG, dU, A, nullptr, dB0, dB1, planes, N, K, M, ld, 2, plan.tn.tile,
-                                                plan.tn.splits},
+                                                plan.tn.splits, low, 1},
                               st);
     return launched(e);
 }

@@ -112,17 +112,21 @@ struct GatedProblem {
 };
 
 // nn: C0 = A0 B0 (+ A1 B1 with parts == 2), A [M, K], B [K, N].
-// tn: C0 = A0^T B0 (and C1 = A1^T B0 with parts == 2), A [K, M], B [K, N].
+// tn: C0 = A0^T B0 (and C1 = A1^T B0 with parts == 2), A [K, M], B [K, N]; with low
+// != 0 the product of the K rows of A `low` elements on with the same B is added.
+// nn with stacked == 2: A's second M / 2 rows are added to the first in the output.
 struct TransposedProblem {
     bool tn;
     const uint16_t *A0, *A1;
     const uint16_t *B0, *B1;
     uint16_t *C0, *C1;
-    float* planes;         // [splits][outputs][M][N], where splits > 1
+    float* planes;         // [splits][outputs][M][N], where splits or stacked > 1
     uint32_t M, N, K;
     uint32_t lda;          // elements between A's rows
     uint32_t parts;
     int tile, splits;      // GatedPlan
+    int64_t low;
+    uint32_t stacked;      // 1 or 2
 };
 
 struct GateGradProblem {
@@ -132,6 +136,7 @@ struct GateGradProblem {
     uint16_t *dG, *dU;     // [M, ld] bf16, ld = N rounded up to a multiple of 8
     uint32_t M, N, ld;
     int act;
+    int64_t low;           // 0, or from dG (dU) to what its rounding leaves
 };
 
 struct W4Operand {
@@ -155,6 +160,11 @@ struct GemvProblem {
 // Pieces of 512 elements (a wave's) of a row of mxfp4_quantize, which numbers those of all rows in 32 bits.
 constexpr uint32_t mx_quant_pieces(uint32_t K) { return K / 512 + (K % 512 != 0); }
 constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 bytes stay within 32-bit offsets
+// Up to this many rows the gated block's gradient keeps 16 bits of dG and dU (two
+// BF16) instead of 8: a gradient of few rows is a sum of few of them, whose
+// roundings then show. It costs nothing there (64-row tiles are half empty, the
+// weights' bytes are the time): 32 x 11008 x 2048 in both.
+constexpr uint32_t kFineRows = 64;
 constexpr uint32_t kMaxGemvK = 1u << 20;      // block / group by one 32-bit multiplication
 constexpr uint32_t kMaxGemvRows = 1u << 16;   // sixteen rows of a grid's y
 constexpr uint32_t kMaxExperts = 1024;   // routing and grouped products

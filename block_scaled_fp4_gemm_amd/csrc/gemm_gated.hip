@@ -56,6 +56,7 @@ struct GatedParams {
     int lda, ldb;           // elements between rows as they lie in memory
     int tiles_m, tiles_n;   // of one product
     int parts;
+    int64_t low;            // tn: 0, or from A to a second A, whose product with the same B is added
     int splits;             // of the reduction's whole steps
     int direct;             // rows start at multiples of 16 bytes: direct loads
 };
@@ -350,7 +351,7 @@ gated_kernel(GatedParams p) {
 
     // the tile's first element of part `part` at reduction index k
     auto a_at = [&](int part, int k) {
-        const uint16_t* a = MODE == MODE_NN && part ? p.A1 : A0;
+        const uint16_t* a = MODE == MODE_NN && part ? p.A1 : MODE == MODE_TN && part ? A0 + p.low : A0;
         return LA == KC ? a + ((int64_t)m0 * p.lda + k) : a + ((int64_t)k * p.lda + m0);
     };
     auto b_at = [&](int part, int k) {
@@ -370,7 +371,7 @@ gated_kernel(GatedParams p) {
     // Steps: the rest of each part by 64 first (guarded), then the whole steps of
     // all parts; the splits take consecutive ones. At most two are guarded, so
     // that they are among the stages that are filled ahead of the loop.
-    const int parts = MODE == MODE_NN ? p.parts : 1;
+    const int parts = MODE == MODE_NN ? p.parts : MODE == MODE_TN && p.low ? 2 : 1;
     const int whole = p.K / STEP, rest = p.K % STEP, guarded = rest ? parts : 0;
     const int each = whole + (rest ? 1 : 0);     // steps of a part
     int first = 0, last = each * parts;
@@ -513,7 +514,9 @@ gated_kernel(GatedParams p) {
 // ---------------------------------------------------------------------------
 // dG = dH U act'(G), dU = dH act(G), with act'(g) = s + g z'(g) s (1 - s).
 // Rows of the results are ld elements apart (a multiple of 8); columns N .. ld-1
-// are written as zeros. Bound by memory: 6 bytes in, 4 out per element.
+// are written as zeros. low != 0: what their rounding to BF16 leaves goes, rounded
+// too, `low` elements behind them. Bound by memory: 10 bytes in, 4 out per
+// element with G and U in FP32.
 // ---------------------------------------------------------------------------
 template <int ACT>
 __device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg, float& du) {
@@ -521,6 +524,12 @@ __device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg,
     const float slope = ACT == BG_SILU ? 1.0f : kGeluC * __builtin_fmaf(3.0f * kGeluK * g, g, 1.0f);
     du = dh * (g * s);
     dg = dh * u * __builtin_fmaf(g * slope, s * (1.0f - s), s);
+}
+
+// What rounding v to r left (nothing where that is no number: r says it all).
+__device__ __forceinline__ float rest(float v, float r) {
+    const float d = v - r;
+    return __builtin_fabsf(d) < __builtin_inff() ? d : 0.0f;
 }
 
 // Eight values p[at ..] of which those below n exist.
@@ -556,7 +565,7 @@ gate_grad_kernel(GateGradProblem p, int64_t chunks) {
         kept8<false>(p.dH, at, left, h);
         kept8<F32>(p.G, at, left, g);
         kept8<F32>(p.U, at, left, u);
-        u32x4 og, ou;
+        u32x4 og, ou, lg, lu;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float g0, g1, u0, u1;
@@ -564,9 +573,16 @@ gate_grad_kernel(GateGradProblem p, int64_t chunks) {
             gate_grad<ACT>(h[2 * e + 1], g[2 * e + 1], u[2 * e + 1], g1, u1);
             og[e] = pack_bf16x2(g0, g1);
             ou[e] = pack_bf16x2(u0, u1);
+            lg[e] = pack_bf16x2(rest(g0, bf16_lo(og[e])), rest(g1, bf16_hi(og[e])));
+            lu[e] = pack_bf16x2(rest(u0, bf16_lo(ou[e])), rest(u1, bf16_hi(ou[e])));
         }
-        *reinterpret_cast<u32x4*>(p.dG + row * p.ld + n) = og;
-        *reinterpret_cast<u32x4*>(p.dU + row * p.ld + n) = ou;
+        uint16_t *dg = p.dG + row * p.ld + n, *du = p.dU + row * p.ld + n;
+        *reinterpret_cast<u32x4*>(dg) = og;
+        *reinterpret_cast<u32x4*>(du) = ou;
+        if (p.low != 0) {
+            *reinterpret_cast<u32x4*>(dg + p.low) = lg;
+            *reinterpret_cast<u32x4*>(du + p.low) = lu;
+        }
     }
 }
 
@@ -662,8 +678,9 @@ hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
     q.ldb = (int)p.N;
     q.parts = (int)p.parts;
     q.splits = (int)p.splits;
+    q.low = p.low;
     q.direct = gated_direct(p.lda) && gated_direct(p.N);
-    if (p.splits == 1) {
+    if (p.splits == 1 && p.stacked == 1) {
         q.C0 = p.C0;
         q.C1 = p.C1;
         return p.tn ? launch_tile<MODE_TN, 0, false>(q, p.tile, stream) : launch_tile<MODE_NN, 0, false>(q, p.tile, stream);
@@ -673,9 +690,10 @@ hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
     q.C1 = p.planes + (size_t)p.M * p.N;
     hipError_t e = p.tn ? launch_tile<MODE_TN, 0, true>(q, p.tile, stream) : launch_tile<MODE_NN, 0, true>(q, p.tile, stream);
     if (e != hipSuccess) return e;
-    const int64_t count = (int64_t)p.M * p.N;
+    // the rows of a plane that are one output's terms are planes of it themselves
+    const int64_t count = (int64_t)(p.M / p.stacked) * p.N;
     hipLaunchKernelGGL(planes_sum_kernel, dim3((unsigned)((count + 1023) / 1024), (unsigned)outputs), dim3(256), 0, stream,
-                       p.planes, p.C0, p.C1, count, q.splits);
+                       p.planes, p.C0, p.C1, count, q.splits * (int)p.stacked);
     return hipGetLastError();
 }
 

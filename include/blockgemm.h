@@ -590,14 +590,15 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
 /*
  * gemm_bf16_gated_backward: the gradients of gemm_bf16_gated for a gradient dH of
  * its result:
- *   dG = bf16(dH * u * act'(g)), dU = bf16(dH * act(g)), on g and u as they were kept;
+ *   dG = bf16(dH * u * act'(g)), dU = bf16(dH * act(g)), on g and u as they were kept
+ *   (both from FP32 products);
  *   dA = bf16(dG B0 + dU B1), dB0 = bf16(dG^T A), dB1 = bf16(dU^T A), FP32 sums.
  *
  *  dH: [M, N], A: [M, K], B0, B1: [N, K] BF16, read.  G, U: [M, N] of kept_type, read.
  *     The roundings of dG and dU are the only ones between FP32 sums with G and U
  *     in FP32: a gradient is then about 1.4 times as far from the exact one (in
  *     the mean) as its own rounding to BF16; kept in BF16, half the memory, 1.8
- *     times.
+ *     times. Up to 64 rows dG and dU enter as two BF16 each, 16 bits of them.
  *  dA: [M, K] or NULL (not wanted; B0 and B1 are then not read).
  *  dB0, dB1: [N, K], or both NULL (A is then not read).
  *  workspace: device buffer of gemm_bf16_gated_backward_workspace(M, N, K) bytes,

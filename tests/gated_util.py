@@ -65,17 +65,19 @@ def check_gated(h, a, b0, b1, act, what):
 
 def check_backward(da, db0, db1, dh, a, b0, b1, g, u, act, what):
     """Against the formula on g and u as they were kept. dG and dU are rounded
-    to BF16 before the products (U16 of their value, besides FP32's few units
-    and the slope's, of which |g| z' s (1 - s) + s <= 3 is the size)."""
+    to BF16 before the products (U16 of their value, or U16 squared up to 64
+    rows, besides FP32's few units and the slope's, of which |g| z' s (1 - s) +
+    s <= 3 is the size)."""
+    low = U16 * U16 if g.shape[0] <= 64 else U16
     dh, a, b0, b1, g, u = (t.double() for t in (dh, a, b0, b1, g, u))
     dg, du = og.gate_grad(dh, g, u, act)
     rel = gate_error(g, act)
-    eg = U16 * dg.abs() + (1 + U16) * rel * 3 * (dh * u).abs() + TINY
-    eu = U16 * du.abs() + (1 + U16) * rel * du.abs() + TINY
+    eg = low * dg.abs() + (1 + U16) * rel * 3 * (dh * u).abs() + TINY
+    eu = low * du.abs() + (1 + U16) * rel * du.abs() + TINY
     want = og.gated_backward(dh, a, b0, b1, g, u, act)
     sizes = (dg.abs() @ b0.abs() + du.abs() @ b1.abs(), dg.abs().T @ a.abs(), du.abs().T @ a.abs())
     errs = (eg @ b0.abs() + eu @ b1.abs(), eg.T @ a.abs(), eu.T @ a.abs())
-    terms = (2 * g.shape[1], g.shape[0], g.shape[0])
+    terms = (4 * g.shape[1], 2 * g.shape[0], 2 * g.shape[0])
     for got, w, size, err, k, name in zip((da, db0, db1), want, sizes, errs, terms, ("dA", "dB0", "dB1")):
         if got is None:
             continue

@@ -69,7 +69,7 @@ def test_split_reduction_is_exact_on_whole_numbers(m, n, k, tile, splits, force)
 
 @pytest.mark.parametrize("kept", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
-@pytest.mark.parametrize("m,n,k", SHAPES + [(1030, 72, 64), (40, 3000, 136)])
+@pytest.mark.parametrize("m,n,k", SHAPES + [(1030, 72, 64), (40, 3000, 136), (33, 1029, 264), (63, 520, 1000)])
 def test_backward(m, n, k, act, kept):
     a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.5 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
     dh = normal((m, n), 0.01, 4)
