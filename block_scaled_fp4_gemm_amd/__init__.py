@@ -780,6 +780,13 @@ def gemm_bf16_gated_backward_workspace(m: int, n: int, k: int) -> int:
     return _bytes_of(lib.gemm_bf16_gated_backward_workspace, "gemm_bf16_gated_backward_workspace", m, n, k)
 
 
+def _given(out, shape, what: str = "out"):
+    """An output that the caller may supply: None, or checked."""
+    if out is not None:
+        _shape(_bits16(out, what), shape, what)
+    return out
+
+
 def _scratch(workspace, need, like: torch.Tensor, stream):
     """(workspace, its bytes): the caller's, or a new one of need() bytes."""
     if workspace is None:
@@ -787,14 +794,7 @@ def _scratch(workspace, need, like: torch.Tensor, stream):
         if nbytes == 0:
             return None, 0
         return _new(like, nbytes, torch.uint8, stream), nbytes
-    return workspace, _tensor(workspace, "workspace").numel() * workspace.element_size()
-
-
-def _out(out, shape, like: torch.Tensor, stream, what: str = "out") -> torch.Tensor:
-    if out is None:
-        return _new(like, shape, torch.bfloat16, stream)
-    _shape(_bits16(out, what), shape, what)
-    return out
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def gemm_bf16_nn(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | None = None,
@@ -804,8 +804,12 @@ def gemm_bf16_nn(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | None = No
     m, k = _dims(_bits16(a, "A"), 2, "A")
     _, n = _dims(_bits16(b, "B"), 2, "B")
     _shape(b, (k, n), "B")
+    _given(out, (m, n))
+    if workspace is not None:
+        _tensor(workspace, "workspace")
     _on_device(a, b, out, workspace)
-    out = _out(out, (m, n), a, stream)
+    if out is None:
+        out = _new(a, (m, n), torch.bfloat16, stream)
     workspace, ws_bytes = _scratch(workspace, lambda: gemm_bf16_nn_workspace(m, n, k), a, stream)
     _check(lib.gemm_bf16_nn(_ptr(a), _ptr(b), _ptr(out), _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
            "gemm_bf16_nn")
@@ -819,8 +823,12 @@ def gemm_bf16_tn(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | None = No
     k, m = _dims(_bits16(a, "A"), 2, "A")
     _, n = _dims(_bits16(b, "B"), 2, "B")
     _shape(b, (k, n), "B")
+    _given(out, (m, n))
+    if workspace is not None:
+        _tensor(workspace, "workspace")
     _on_device(a, b, out, workspace)
-    out = _out(out, (m, n), a, stream)
+    if out is None:
+        out = _new(a, (m, n), torch.bfloat16, stream)
     workspace, ws_bytes = _scratch(workspace, lambda: gemm_bf16_tn_workspace(m, n, k), a, stream)
     _check(lib.gemm_bf16_tn(_ptr(a), _ptr(b), _ptr(out), _ptr(workspace), ws_bytes, m, n, k, _stream(stream)),
            "gemm_bf16_tn")
@@ -837,8 +845,10 @@ def gemm_bf16_gated(a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, act: st
     n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
     _shape(b0, (n, k), "B0")
     _shape(_bits16(b1, "B1"), (n, k), "B1")
+    _given(out, (m, n))
     _on_device(a, b0, b1, out)
-    out = _out(out, (m, n), a, stream)
+    if out is None:
+        out = _new(a, (m, n), torch.bfloat16, stream)
     kept = torch.float32 if save is True else save
     g, u = (_new(a, (m, n), kept, stream) for _ in range(2)) if save else (None, None)
     _check(lib.gemm_bf16_gated(_ptr(a), _ptr(b0), _ptr(b1), _ptr(out), _ptr(g), _ptr(u), _type(g, "save") if save else 0,
@@ -864,6 +874,8 @@ def gemm_bf16_gated_backward(dh: torch.Tensor, a: torch.Tensor, b0: torch.Tensor
     if _type(u, "U") != kept:
         raise TypeError(f"U: expected {g.dtype}, got {u.dtype}")
     _shape(u, (m, n), "U")
+    if workspace is not None:
+        _tensor(workspace, "workspace")
     _on_device(dh, a, b0, b1, g, u, workspace)
     da = _new(a, (m, k), torch.bfloat16, stream) if need_a else None
     db0, db1 = (_new(a, (n, k), torch.bfloat16, stream) for _ in range(2)) if need_b else (None, None)
@@ -931,8 +943,10 @@ def gemv_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, stre
     """Y[R,N] = bf16(x[R,K] @ deq(W)^T) for few rows of bfloat16 activations (16 at a time)."""
     r, k = _dims(_bits16(x, "x"), 2, "x")
     held, n = _w4(w, k, "W")
+    _given(out, (r, n))
     _on_device(x, out)
-    out = _out(out, (r, n), x, stream)
+    if out is None:
+        out = _new(x, (r, n), torch.bfloat16, stream)
     _check(lib.gemv_w4(_ptr(x), ctypes.byref(held), _ptr(out), r, n, k, _stream(stream)), "gemv_w4")
     return out
 
@@ -946,8 +960,10 @@ def gemv_w4_gated(x: torch.Tensor, w0: W4Weights, w1: W4Weights, act: str = "sil
     held1, n1 = _w4(w1, k, "W1")
     if n1 != n or held1.format != held0.format or held1.group != held0.group or (w0.zeros is None) != (w1.zeros is None):
         raise ValueError("W0 and W1 must have the same shape, format and group, both or neither zeros")
+    _given(out, (r, n))
     _on_device(x, out)
-    out = _out(out, (r, n), x, stream)
+    if out is None:
+        out = _new(x, (r, n), torch.bfloat16, stream)
     _check(lib.gemv_w4_gated(_ptr(x), ctypes.byref(held0), ctypes.byref(held1), _ptr(out), kind, r, n, k,
                              _stream(stream)), "gemv_w4_gated")
     return out

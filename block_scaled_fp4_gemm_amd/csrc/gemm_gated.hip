@@ -287,34 +287,6 @@ __device__ __forceinline__ void store_tile(OUT* C, int64_t ldc, int M, int N, in
     }
 }
 
-// FP32 results straight from the accumulators: a lane's four columns are 16 bytes,
-// two lanes' 32 consecutive bytes of a row, and the next stores complete the lines.
-template <int BM, int BNO, int WM, int WN, int FM, int JN, class Value>
-__device__ __forceinline__ void store_direct(float* C, int64_t ldc, int M, int N, int m0, int n0, int wm, int wn, int lane,
-                                             Value&& value) {
-    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int m = m0 + wm * (BM / WM) + i * 32 + (lane & 31);
-        if (m >= M) continue;
-#pragma unroll
-        for (int j = 0; j < JN; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int n = n0 + wn * (BNO / WN) + j * 32 + g * 8 + (lane >> 5) * 4;
-                float* dst = C + (int64_t)m * ldc + n;
-                const f32x4 v = {value(i, j, 4 * g), value(i, j, 4 * g + 1), value(i, j, 4 * g + 2), value(i, j, 4 * g + 3)};
-                if (n + 4 <= N) {
-                    *reinterpret_cast<f32x4_any*>(dst) = v;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < N) dst[e] = v[e];
-                }
-            }
-    }
-}
-
 // STAGES == 1: every step guarded, for rows that do not start at multiples of 16 bytes.
 template <int MODE, int ACT, int BM, int BN, int WM, int WN, int STAGES, bool PLANES>
 __global__ void __launch_bounds__(WM * WN * 64)
@@ -489,8 +461,8 @@ gated_kernel(GatedParams p) {
             auto g = [&](int i, int j, int e) { return acc[i][2 * j][e]; };
             auto u = [&](int i, int j, int e) { return acc[i][2 * j + 1][e]; };
             if (p.kept == BG_F32) {
-                store_direct<BM, BNO, WM, WN, FM, FN / 2>(static_cast<float*>(p.G), p.N, p.M, p.N, m0, n0, wm, wn, elane, g);
-                store_direct<BM, BNO, WM, WN, FM, FN / 2>(static_cast<float*>(p.U), p.N, p.M, p.N, m0, n0, wm, wn, elane, u);
+                out(static_cast<float*>(p.G), g);
+                out(static_cast<float*>(p.U), u);
             } else {
                 out(static_cast<uint16_t*>(p.G), g);
                 out(static_cast<uint16_t*>(p.U), u);
