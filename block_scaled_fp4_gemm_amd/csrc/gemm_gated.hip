@@ -493,9 +493,11 @@ gated_kernel(GatedParams p) {
 template <int ACT>
 __device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg, float& du) {
     const float s = gate_sigmoid<ACT>(g);
-    const float slope = ACT == BG_SILU ? 1.0f : kGeluC * __builtin_fmaf(3.0f * kGeluK * g, g, 1.0f);
+    // past 10^4 s (1 - s) is 0, and must not meet an overflow
+    const float c = __builtin_fminf(__builtin_fmaxf(g, -1e4f), 1e4f);
+    const float slope = ACT == BG_SILU ? 1.0f : kGeluC * __builtin_fmaf(3.0f * kGeluK * c, c, 1.0f);
     du = dh * (g * s);
-    dg = dh * u * __builtin_fmaf(g * slope, s * (1.0f - s), s);
+    dg = dh * u * __builtin_fmaf(c * slope, s * (1.0f - s), s);
 }
 
 // What rounding v to r left (nothing where that is no number: r says it all).
