@@ -50,10 +50,11 @@ uint32_t pitch8(uint32_t n) { return (n + 7) / 8 * 8; }
 
 // An nn (C [M, N] of K terms, parts of them) or tn (parts outputs) product, A's
 // rows lda elements apart.
-GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t lda, uint32_t parts, uint32_t cus) {
+GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t lda, uint32_t parts, uint32_t cus,
+                          double* us = nullptr) {
     const bool direct = gated_direct(lda) && gated_direct(N);
     const uint32_t steps = direct ? K / 64 : K / 64 + (K % 64 != 0);
-    return plan_of(false, tn, direct, M, N, tn ? steps : steps * parts, tn ? parts : 1, cus, tune(BG_TUNE_TILE));
+    return plan_of(false, tn, direct, M, N, tn ? steps : steps * parts, tn ? parts : 1, cus, tune(BG_TUNE_TILE), us);
 }
 uint64_t planes_bytes(const GatedPlan& p, uint32_t M, uint32_t N, uint32_t outputs) {
     return p.splits > 1 ? (uint64_t)p.splits * outputs * M * N * 4 : 0;
@@ -102,22 +103,37 @@ bool gated_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
 }
 
 // The gradient's workspace: dG and dU, each followed by its low half where M is
-// small, then the larger of the two products' planes.
+// small, then the products' planes: both products' where one launch takes them
+// (pair; a product that is wanted alone keeps its plan), else the larger of the two.
 struct GradPlan {
     GatedPlan nn, tn;
+    bool pair;
     uint32_t stacked;        // 2 with low halves: dA's product runs over both as 2 M rows
     uint64_t half, bytes;    // of dG (with its low half); of all
+    uint64_t nn_planes;      // bytes, where both are kept
 };
 GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
     GradPlan g;
+    double us_nn = 0, us_tn = 0;
     g.stacked = M <= kFineRows ? 2 : 1;
-    g.nn = transposed_plan(false, M * g.stacked, K, N, pitch8(N), 2, cus);
-    g.tn = transposed_plan(true, N, K, M, pitch8(N), 2, cus);
+    g.nn = transposed_plan(false, M * g.stacked, K, N, pitch8(N), 2, cus, &us_nn);
+    g.tn = transposed_plan(true, N, K, M, pitch8(N), 2, cus, &us_tn);
     g.half = (uint64_t)M * pitch8(N) * 2 * g.stacked;
+    g.pair = false;
+    if (gated_direct(pitch8(N)) && gated_direct(K) && tune(BG_TUNE_TILE) < 0) {
+        // a launch and the wait for the one before it take about 3 us
+        const PairPlan p = pair_plan({M * g.stacked, N}, {K, K}, {N / 64 * 2, M / 64 * g.stacked}, {1, 2}, g.stacked, cus);
+        if (p.nn != 0 && p.us < us_nn + us_tn + 3.0) {
+            g.pair = true;
+            g.nn = GatedPlan{GT_128x128_DEEP, p.nn};
+            g.tn = GatedPlan{GT_128x128_DEEP, p.tn};
+        }
+    }
     const uint64_t rows = (uint64_t)M * g.stacked;
-    const uint64_t a = g.nn.splits > 1 || g.stacked > 1 ? (uint64_t)g.nn.splits * rows * K * 4 : 0;
+    const uint64_t a = g.nn.splits > 1 || g.stacked > 1 ? ((uint64_t)g.nn.splits * rows * K * 4 + 15) / 16 * 16 : 0;
     const uint64_t b = planes_bytes(g.tn, N, K, 2);
-    g.bytes = 2 * g.half + (a > b ? a : b);
+    g.nn_planes = g.pair ? a : 0;
+    g.bytes = 2 * g.half + (g.pair ? a + b : a > b ? a : b);
     return g;
 }
 
@@ -242,6 +258,7 @@ bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const 
     if (s != BG_OK) return s;
     uint32_t cus = 0;
     if ((s = check_device(&cus)) != BG_OK) return s;
+    const bool want_a = dA != nullptr && M != 0 && K != 0, want_b = dB0 != nullptr && N != 0 && K != 0;
     const GradPlan plan = grad_plan(M, N, K, cus);
     if (plan.bytes != 0) {
         if (workspace == nullptr || workspace_bytes < plan.bytes) return BG_ERR_WORKSPACE;
@@ -254,18 +271,19 @@ bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const 
     float* planes = reinterpret_cast<float*>(dU + plan.half / 2);
     const uint32_t ld = pitch8(N);
     const int64_t low = plan.stacked > 1 ? (int64_t)M * ld : 0;
-    const bool want_a = dA != nullptr && M != 0 && K != 0, want_b = dB0 != nullptr && N != 0 && K != 0;
     if (!want_a && !want_b) return BG_OK;
     hipError_t e = hipSuccess;
     if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, kept_type, dG, dU, M, N, ld, act, low}, st);
-    if (e == hipSuccess && want_a)
-        e = launch_transposed(TransposedProblem{false, dG, dU, B0, B1, dA, nullptr, planes, M * plan.stacked, K, N, ld, 2,
-                                                plan.nn.tile, plan.nn.splits, 0, plan.stacked},
-                              st);
-    if (e == hipSuccess && want_b)
-        e = launch_transposed(TransposedProblem{true, dG, dU, A, nullptr, dB0, dB1, planes, N, K, M, ld, 2, plan.tn.tile,
-                                                plan.tn.splits, low, 1},
-                              st);
+    const TransposedProblem nn{false, dG, dU, B0, B1, dA, nullptr, planes, M * plan.stacked, K, N, ld, 2, plan.nn.tile,
+                               plan.nn.splits, 0, plan.stacked};
+    const TransposedProblem tn{true, dG, dU, A, nullptr, dB0, dB1, planes + plan.nn_planes / 4, N, K, M, ld, 2, plan.tn.tile,
+                               plan.tn.splits, low, 1};
+    if (plan.pair && want_a && want_b) {
+        if (e == hipSuccess) e = launch_transposed_pair(nn, tn, st);
+    } else {
+        if (e == hipSuccess && want_a) e = launch_transposed(nn, st);
+        if (e == hipSuccess && want_b) e = launch_transposed(tn, st);
+    }
     return launched(e);
 }
 

@@ -248,6 +248,8 @@ hipError_t launch_moe_route_backward(const RouteBackwardProblem& p, hipStream_t 
 
 hipError_t launch_gated(const GatedProblem& p, hipStream_t stream);
 hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream);
+// Both in one launch: 128 x 128 tiles, direct loads, planes of their own.
+hipError_t launch_transposed_pair(const TransposedProblem& nn, const TransposedProblem& tn, hipStream_t stream);
 hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t stream);
 hipError_t launch_gemv_w4(const GemvProblem& p, hipStream_t stream);
 

@@ -75,7 +75,7 @@ constexpr int kMaxSplits = 16;
 // workspace: one), whose time by the table is least. Without direct loads there is
 // one tile (kGuarded). `forced` >= 0: tile forced % 16 and forced / 16 parts.
 inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t N, uint32_t steps, uint32_t outputs, uint32_t cus,
-                         int forced) {
+                         int forced, double* time = nullptr) {
     const int most = steps < 2 ? 1 : steps < (uint32_t)kMaxSplits ? (int)steps : kMaxSplits;
     auto ok = [&](const GatedPlan& p) {
         return !(tn && p.tile == GT_160x256) && (p.tile == GT_256x256 || gated_launches(p, gated, M, N, outputs));
@@ -99,6 +99,34 @@ inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t 
             const double us = gated_us(info, n * splits, (double)gated_ceil(steps ? steps : 1, splits), cus) +
                               planes_us(M, N, outputs, splits);
             if (least < 0 || us < least) best = p, least = us;
+        }
+    }
+    if (time != nullptr) *time = least;
+    return best;
+}
+
+// An nn and a tn product in one launch of GT_128x128_DEEP tiles, where all their
+// workgroups run at once: the parts of each whose longer time is least, with the
+// us; splits 0 where they do not fit. m, n, steps, outputs: of each product.
+struct PairPlan {
+    int nn, tn;
+    double us;
+};
+inline PairPlan pair_plan(const uint32_t (&m)[2], const uint32_t (&n)[2], const uint32_t (&steps)[2], const uint32_t (&outputs)[2],
+                          uint32_t stacked, uint32_t cus) {
+    const GatedTileInfo& t = kGatedTiles[GT_128x128_DEEP];
+    uint64_t tiles[2];
+    for (int i = 0; i < 2; ++i) tiles[i] = gated_tiles(GT_128x128_DEEP, false, m[i], n[i], outputs[i]);
+    PairPlan best{0, 0, 0};
+    for (uint32_t a = 1; a <= (uint32_t)kMaxSplits && tiles[0] * a < cus; ++a) {
+        if (a > 1 && steps[0] / a < 4) break;
+        for (uint32_t b = 1; b <= (uint32_t)kMaxSplits && tiles[0] * a + tiles[1] * b <= cus; ++b) {
+            if (b > 1 && steps[1] / b < 4) break;
+            const double sa = (double)gated_ceil(steps[0] ? steps[0] : 1, a), sb = (double)gated_ceil(steps[1] ? steps[1] : 1, b);
+            const double us = t.fixed + t.full * (sa > sb ? sa : sb) +
+                              (a > 1 || stacked > 1 ? planes_us(m[0], n[0], outputs[0], (int)a + 1) : 0.0) +
+                              planes_us(m[1], n[1], outputs[1], (int)b);
+            if (best.nn == 0 || us < best.us) best = PairPlan{(int)a, (int)b, us};
         }
     }
     return best;

@@ -289,21 +289,19 @@ __device__ __forceinline__ void store_tile(OUT* C, int64_t ldc, int M, int N, in
 
 // STAGES == 1: every step guarded, for rows that do not start at multiples of 16 bytes.
 template <int MODE, int ACT, int BM, int BN, int WM, int WN, int STAGES, bool PLANES>
-__global__ void __launch_bounds__(WM * WN * 64)
-gated_kernel(GatedParams p) {
+__device__ __forceinline__ void gated_body(const GatedParams& p, uint16_t* smem, int tile, int split) {
     constexpr bool PAIR = MODE == MODE_GATED;
     constexpr int LA = MODE == MODE_TN ? MC : KC, LB = MODE == MODE_GATED ? KC : MC;
     constexpr int NT = WM * WN * 64, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
     static_assert(FM * 32 * WM == BM && FN * 32 * WN == BN && (!PAIR || FN % 2 == 0), "whole fragments, pairs of them");
     constexpr int STAGE = (BM + BN) * STEP;
     constexpr int BNO = PAIR ? BN / 2 : BN;       // output columns
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[STAGES * STAGE];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
     int tm, tn;
-    tile_of<ORDER_GEMM>((int)blockIdx.x, MODE == MODE_TN ? p.tiles_m * p.parts : p.tiles_m, p.tiles_n, tm, tn);
+    tile_of<ORDER_GEMM>(tile, MODE == MODE_TN ? p.tiles_m * p.parts : p.tiles_m, p.tiles_n, tm, tn);
     const uint16_t* A0 = p.A0;
     void* C = p.C0;
     if (MODE == MODE_TN && tm >= p.tiles_m) {     // the second product
@@ -349,7 +347,7 @@ gated_kernel(GatedParams p) {
     int first = 0, last = each * parts;
     if constexpr (PLANES) {
         const int per = (last + p.splits - 1) / p.splits;
-        first = min((int)blockIdx.y * per, last);
+        first = min(split * per, last);
         last = min(first + per, last);
     }
     const int nsteps = last - first;
@@ -473,7 +471,7 @@ gated_kernel(GatedParams p) {
         auto value = [&](int i, int j, int e) { return acc[i][j][e]; };
         if constexpr (PLANES) {
             const int64_t rows = MODE == MODE_TN ? (int64_t)p.M * p.parts : p.M;
-            float* plane = static_cast<float*>(p.C0) + (int64_t)blockIdx.y * rows * p.N;
+            float* plane = static_cast<float*>(p.C0) + (int64_t)split * rows * p.N;
             if (MODE == MODE_TN && C != p.C0) plane += (int64_t)p.M * p.N;
             store_tile<float, false, BM, BNO, WM, WN, FM, FN, NT, CAP>(plane, p.N, p.M, p.N, m0, n0, lds, wm, wn, elane, etid, value);
         } else {
@@ -481,6 +479,26 @@ gated_kernel(GatedParams p) {
                                                                   wn, elane, etid, value);
         }
     }
+}
+
+template <int MODE, int ACT, int BM, int BN, int WM, int WN, int STAGES, bool PLANES>
+__global__ void __launch_bounds__(WM * WN * 64)
+gated_kernel(GatedParams p) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[STAGES * (BM + BN) * STEP];
+    gated_body<MODE, ACT, BM, BN, WM, WN, STAGES, PLANES>(p, smem, (int)blockIdx.x, (int)blockIdx.y);
+}
+
+// An nn and a tn product that do not wait for each other, in one launch: the first
+// workgroups take a's tiles (split by split), the others b's.
+template <int BM, int BN, int WM, int WN, int STAGES, bool PLANES_A, bool PLANES_B>
+__global__ void __launch_bounds__(WM * WN * 64)
+pair_kernel(GatedParams a, GatedParams b, int tiles_a, int blocks_a, int tiles_b) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[STAGES * (BM + BN) * STEP];
+    const int i = (int)blockIdx.x;
+    if (i < blocks_a)
+        gated_body<MODE_NN, 0, BM, BN, WM, WN, STAGES, PLANES_A>(a, smem, i % tiles_a, i / tiles_a);
+    else
+        gated_body<MODE_TN, 0, BM, BN, WM, WN, STAGES, PLANES_B>(b, smem, (i - blocks_a) % tiles_b, (i - blocks_a) / tiles_b);
 }
 
 // ---------------------------------------------------------------------------
@@ -639,8 +657,9 @@ hipError_t launch_gated(const GatedProblem& p, hipStream_t stream) {
                             : launch_tile<MODE_GATED, BG_GELU_TANH, false>(q, p.tile, stream);
 }
 
-hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
-    GatedParams q{};
+// Whether the product goes through planes, and its parameters.
+static bool transposed_params(const TransposedProblem& p, GatedParams& q) {
+    q = GatedParams{};
     q.A0 = p.A0;
     q.A1 = p.A1;
     q.B0 = p.B0;
@@ -654,21 +673,45 @@ hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
     q.splits = (int)p.splits;
     q.low = p.low;
     q.direct = gated_direct(p.lda) && gated_direct(p.N);
-    if (p.splits == 1 && p.stacked == 1) {
-        q.C0 = p.C0;
-        q.C1 = p.C1;
-        return p.tn ? launch_tile<MODE_TN, 0, false>(q, p.tile, stream) : launch_tile<MODE_NN, 0, false>(q, p.tile, stream);
-    }
-    const int outputs = p.tn ? (int)p.parts : 1;
-    q.C0 = p.planes;
-    q.C1 = p.planes + (size_t)p.M * p.N;
-    hipError_t e = p.tn ? launch_tile<MODE_TN, 0, true>(q, p.tile, stream) : launch_tile<MODE_NN, 0, true>(q, p.tile, stream);
-    if (e != hipSuccess) return e;
+    const bool planes = p.splits > 1 || p.stacked > 1;
+    q.C0 = planes ? static_cast<void*>(p.planes) : p.C0;
+    q.C1 = planes ? static_cast<void*>(p.planes + (size_t)p.M * p.N) : p.C1;
+    return planes;
+}
+
+static hipError_t launch_planes_sum(const TransposedProblem& p, hipStream_t stream) {
     // the rows of a plane that are one output's terms are planes of it themselves
     const int64_t count = (int64_t)(p.M / p.stacked) * p.N;
-    hipLaunchKernelGGL(planes_sum_kernel, dim3((unsigned)((count + 1023) / 1024), (unsigned)outputs), dim3(256), 0, stream,
-                       p.planes, p.C0, p.C1, count, q.splits * (int)p.stacked);
+    hipLaunchKernelGGL(planes_sum_kernel, dim3((unsigned)((count + 1023) / 1024), p.tn ? (unsigned)p.parts : 1u), dim3(256), 0,
+                       stream, p.planes, p.C0, p.C1, count, p.splits * (int)p.stacked);
     return hipGetLastError();
+}
+
+hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
+    GatedParams q;
+    if (!transposed_params(p, q))
+        return p.tn ? launch_tile<MODE_TN, 0, false>(q, p.tile, stream) : launch_tile<MODE_NN, 0, false>(q, p.tile, stream);
+    const hipError_t e =
+        p.tn ? launch_tile<MODE_TN, 0, true>(q, p.tile, stream) : launch_tile<MODE_NN, 0, true>(q, p.tile, stream);
+    return e != hipSuccess ? e : launch_planes_sum(p, stream);
+}
+
+hipError_t launch_transposed_pair(const TransposedProblem& nn, const TransposedProblem& tn, hipStream_t stream) {
+    GatedParams a, b;
+    const bool pa = transposed_params(nn, a), pb = transposed_params(tn, b);
+    constexpr int BM = 128, BN = 128;      // GT_128x128_DEEP
+    for (GatedParams* q : {&a, &b}) {
+        q->tiles_m = (q->M + BM - 1) / BM;
+        q->tiles_n = (q->N + BN - 1) / BN;
+    }
+    const int ta = a.tiles_m * a.tiles_n, tb = b.tiles_m * b.tiles_n * b.parts, ba = ta * a.splits;
+    auto k = pa ? (pb ? pair_kernel<BM, BN, 4, 2, 4, true, true> : pair_kernel<BM, BN, 4, 2, 4, true, false>)
+                : (pb ? pair_kernel<BM, BN, 4, 2, 4, false, true> : pair_kernel<BM, BN, 4, 2, 4, false, false>);
+    k<<<dim3((unsigned)(ba + tb * b.splits)), dim3(512), 0, stream>>>(a, b, ta, ba, tb);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && pa) e = launch_planes_sum(nn, stream);
+    if (e == hipSuccess && pb) e = launch_planes_sum(tn, stream);
+    return e;
 }
 
 hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t stream) {

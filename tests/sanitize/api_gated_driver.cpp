@@ -59,6 +59,15 @@ hipError_t launch_transposed(const TransposedProblem& p, hipStream_t) {
     ++g_launches;
     return hipSuccess;
 }
+hipError_t launch_transposed_pair(const TransposedProblem& nn, const TransposedProblem& tn, hipStream_t s) {
+    CHECK(!nn.tn && tn.tn && nn.tile == GT_128x128_DEEP && tn.tile == GT_128x128_DEEP);
+    // all workgroups at once, planes that do not meet
+    CHECK(gated_tiles(nn.tile, false, nn.M, nn.N, 1) * nn.splits + gated_tiles(tn.tile, false, tn.M, tn.N, 2) * tn.splits <= 256);
+    CHECK(tn.planes >= nn.planes + (nn.splits > 1 || nn.stacked > 1 ? (uint64_t)nn.splits * nn.M * nn.N : 0));
+    (void)launch_transposed(nn, s);
+    (void)launch_transposed(tn, s);
+    return hipSuccess;
+}
 hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t) {
     CHECK(p.M > 0 && p.N > 0 && p.ld % 8 == 0 && p.ld >= p.N && p.ld < p.N + 8);
     inside(p.dG, (uint64_t)p.M * p.ld * 2 + 2 * p.low);
