@@ -1,7 +1,7 @@
 // Products of few rows with weights in 4 bits and group scales, and the gated
 // MLP block of few rows: y = x W^T, h = act(x W0^T) * (x W1^T).
 //
-// A wave takes 16 weight rows and a stretch of K. Per 128 elements of K every
+// A wave takes 16 weight rows and stretches of K. Per 128 elements of K every
 // lane loads 16 bytes of codes (32 elements of one row: lane l has row l % 16,
 // part l / 16), converts them to BF16 exactly, and four 16x16x32 matrix
 // instructions multiply them with up to 16 rows of x. K's order inside the
@@ -18,6 +18,17 @@
 //          there the lanes exchange their words first (a 4 x 4 transposition
 //          over the wave's four parts), so that an instruction covers 32
 //          consecutive elements.
+//
+// Bound by the weights' bytes, and for more rows by x, which every workgroup
+// reads whole: 7168 x 16384 MXFP4 (62 MB) takes 15.1 us for one row (4.1 TB/s; the
+// codes alone, read the same way without a use, take 10.7) and 21.8 us for 16,
+// where 224 workgroups read 115 MB of x besides (16.0 us without that). What
+// made it so, one row and 16: x loaded from global memory by every wave 27 and
+// 51 us (its loads wait behind the codes', which the counter retires in order);
+// through LDS, one chunk of K for all waves, 38 and 43 us with scales loaded and
+// shifted where they are read (the next loads waited for them); with scales of
+// four blocks in one load and nothing between the loads 15 and 22 us. Codes two
+// stretches ahead instead of one gain nothing (14.6 and 22.2 us, and short K lose).
 #include <type_traits>
 
 #include "bg_internal.hpp"
@@ -259,7 +270,8 @@ gemv_w4_kernel(GemvParams p) {
                     }
 #pragma unroll
                     for (int s = 0; s < SETS; ++s) {
-                        const uint32_t h = scale[s][g / GB][b];
+                        // past the end of K the group read is another one, perhaps infinite
+                        const uint32_t h = k0 + b * BLOCK + g * 32 < p.K ? scale[s][g / GB][b] : 0u;
                         const float by = bf16_hi(h), off = 16.0f + (float)(h & 0xFFFFu);
 #pragma unroll
                         for (int e = 0; e < (RP == 1 ? 1 : 4); ++e)      // row 0 is element 0

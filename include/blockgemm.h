@@ -716,7 +716,10 @@ const char* bg_status_string(bg_status status);
  *
  *  BG_TUNE_TILE:       dense tile configuration (gemm_bf16 and the entry
  *                      points built on it: dual, strided, scaled_acc,
- *                      split-K planes), an index into the library's tile table
+ *                      split-K planes), an index into the library's tile table;
+ *                      gemm_bf16_gated, _nn, _tn and _gated_backward: index
+ *                      into their own table, plus 16 times the number of parts
+ *                      of the reduction (nn, tn; 0 is one)
  *  BG_TUNE_COLSPLIT:   0 turns the column split of gemm_bf16 off
  *  BG_TUNE_ORDERED:    variant of gemm_bf16_ordered (0-11 register blocks of
  *                      the tile form, 12-14 the scalar-A form with 1-3 rows
