@@ -546,7 +546,10 @@ __device__ __forceinline__ void kept8(const void* p, int64_t at, int n, float (&
         typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
         const float* q = static_cast<const float*>(p) + at;
         if (n >= 8) {
-            const f32x4 a = *reinterpret_cast<const f32x4_any*>(q), b = *reinterpret_cast<const f32x4_any*>(q + 4);
+            // read once, and more than the caches hold where it is long: past them the
+            // gradient of 5120 x 11008 x 2048 takes 940 instead of 946 us
+            const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(q));
+            const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(q + 4));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = a[e], v[e + 4] = b[e];
         } else {
