@@ -93,7 +93,7 @@ bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C,
         if ((s = check_operands(with, planes)) != BG_OK) return s;
     }
     return launched(launch_transposed(TransposedProblem{tn, A, nullptr, B, nullptr, C, nullptr, static_cast<float*>(ws), M, N, K,
-                                                        tn ? M : K, 1, plan.tile, plan.splits, 0, 1},
+                                                        tn ? M : K, 1, plan.tile, plan.splits, 0, 1, plan.wide},
                                       (hipStream_t)stream));
 }
 
@@ -215,7 +215,7 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
     uint32_t cus = 0;
     if ((s = check_device(&cus)) != BG_OK) return s;
     const GatedPlan plan = plan_of(true, false, gated_direct(K), M, N, K / 64, 1, cus, tune(BG_TUNE_TILE));
-    return launched(launch_gated(GatedProblem{A, B0, B1, H, G, U, kept_type, M, N, K, act, plan.tile}, (hipStream_t)stream));
+    return launched(launch_gated(GatedProblem{A, B0, B1, H, G, U, kept_type, M, N, K, act, plan.tile, plan.wide}, (hipStream_t)stream));
 }
 
 bg_status gemm_bf16_nn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
@@ -275,9 +275,9 @@ bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const 
     hipError_t e = hipSuccess;
     if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, kept_type, dG, dU, M, N, ld, act, low}, st);
     const TransposedProblem nn{false, dG, dU, B0, B1, dA, nullptr, planes, M * plan.stacked, K, N, ld, 2, plan.nn.tile,
-                               plan.nn.splits, 0, plan.stacked};
+                               plan.nn.splits, 0, plan.stacked, plan.nn.wide};
     const TransposedProblem tn{true, dG, dU, A, nullptr, dB0, dB1, planes + plan.nn_planes / 4, N, K, M, ld, 2, plan.tn.tile,
-                               plan.tn.splits, low, 1};
+                               plan.tn.splits, low, 1, plan.tn.wide};
     if (plan.pair && want_a && want_b) {
         if (e == hipSuccess) e = launch_transposed_pair(nn, tn, st);
     } else {

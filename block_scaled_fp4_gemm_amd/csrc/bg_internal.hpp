@@ -108,7 +108,8 @@ struct GatedProblem {
     int kept;              // bg_type
     uint32_t M, N, K;
     int act;               // bg_activation
-    int tile;              // GatedTile
+    int tile;              // GatedPlan
+    uint32_t wide;
 };
 
 // nn: C0 = A0 B0 (+ A1 B1 with parts == 2), A [M, K], B [K, N].
@@ -127,6 +128,7 @@ struct TransposedProblem {
     int tile, splits;      // GatedPlan
     int64_t low;
     uint32_t stacked;      // 1 or 2
+    uint32_t wide;         // GatedPlan
 };
 
 struct GateGradProblem {

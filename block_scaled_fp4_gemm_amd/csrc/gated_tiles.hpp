@@ -15,13 +15,15 @@ struct GatedTileInfo {
     int bm, bn, threads;
     double fixed, few, full, pair_fixed, pair;
 };
-enum GatedTile : int { GT_256x256, GT_160x256, GT_256x128, GT_128x128, GT_128x128_DEEP, GT_64x128, GT_TILES };
+enum GatedTile : int { GT_256x256, GT_160x256, GT_256x128, GT_128x128, GT_128x128_DEEP, GT_64x128, GT_MIXED, GT_TILES };
 constexpr GatedTileInfo kGatedTiles[GT_TILES] = {{256, 256, 512, 9.0, 1.25, 1.72, 0, 0},
                                                  {160, 256, 256, 7.5, 0.80, 1.20, 0, 0},
                                                  {256, 128, 512, 5.7, 0.68, 1.04, 0, 0},
                                                  {128, 128, 256, 4.0, 0.70, 0.78, 5.0, 1.02},
                                                  {128, 128, 512, 4.8, 0.41, 0.58, 0, 0},
-                                                 {64, 128, 256, 4.4, 0.48, 0.52, 4.6, 0.69}};
+                                                 {64, 128, 256, 4.4, 0.48, 0.52, 4.6, 0.69},
+                                                 // 256 x 256 tiles, the last columns in 256 x 128: counted as the latter
+                                                 {256, 128, 512, 0, 0, 0, 0, 0}};
 
 // Rows that do not start at multiples of 16 bytes: 128 x 128 tiles, every step
 // loaded through registers with checks.
@@ -36,6 +38,7 @@ inline bool gated_direct(uint32_t ld) { return ld % 8 == 0 && (uint64_t)ld * 512
 
 struct GatedPlan {
     int tile, splits;
+    uint32_t wide = 0;      // GT_MIXED: columns of 256 x 256 tiles
 };
 
 inline uint64_t gated_ceil(uint64_t n, uint64_t by) { return (n + by - 1) / by; }
@@ -63,6 +66,30 @@ inline double gated_us(const GatedTileInfo& t, uint64_t n, double steps, uint32_
     return us;
 }
 
+// GT_MIXED: whole rounds of 256 x 256 tiles (`fewer`: one less than there are); the
+// columns that are left go in 256 x 128 tiles, first on the units that the last
+// round leaves free. It saves most of a round that 256 x 256 tiles alone would
+// fill to less than a half: 5120 x 11008 x 2048 as nn (860 of them, 3.4 rounds)
+// 200 us, in 256 x 256 alone 248, in 256 x 128 alone 230; 2048 x 11008 x 5120 as
+// tn (344, 1.3 rounds) 200, 236, 234 us. One round less pays where the columns do
+// not divide the rounds: 12152 x 2672 x 5736 as tn 340 us, with the other rule 384.
+inline uint32_t mixed_columns(bool gated, uint32_t M, uint32_t N, uint32_t outputs, uint32_t cus, bool fewer) {
+    const uint64_t column = gated_ceil(M, 256) * outputs, all = gated_ceil(N, tile_columns(256, gated));
+    const uint64_t rounds = column * all / cus;
+    if (rounds < (fewer ? 2 : 1)) return 0;
+    return (uint32_t)((rounds - (fewer ? 1 : 0)) * cus / column);
+}
+inline double mixed_us(bool gated, uint32_t M, uint32_t N, double steps, uint32_t outputs, uint32_t cus, uint32_t wide) {
+    const GatedTileInfo &w = kGatedTiles[GT_256x256], &t = kGatedTiles[GT_256x128];
+    const uint64_t column = gated_ceil(M, 256) * outputs, done = (uint64_t)wide * tile_columns(256, gated);
+    const uint64_t wides = column * wide, narrow = column * (done < N ? gated_ceil(N - done, tile_columns(128, gated)) : 0);
+    const double round = w.fixed + steps * w.full;
+    const uint64_t last = wides % cus, free = last ? cus - last : 0;      // of the last round
+    double us = (double)gated_ceil(wides, cus) * round;
+    const uint64_t beside = free * (uint64_t)(round / (t.fixed + steps * t.full));
+    return us + (narrow > beside ? gated_us(t, narrow - beside, steps, cus) : 0.0);
+}
+
 // The planes of a split reduction: written by the product and read by their sum
 // (at about 4 bytes a ps), and the second launch.
 inline double planes_us(uint32_t M, uint32_t N, uint32_t outputs, int splits) {
@@ -83,12 +110,13 @@ inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t 
     if (forced >= 0) {
         GatedPlan p{forced % 16 < GT_TILES ? forced % 16 : GT_256x256, 1};
         if (!gated && forced >= 16) p.splits = forced / 16 < most ? forced / 16 : most;
+        if (p.tile == GT_MIXED) p.splits = 1, p.wide = (uint32_t)(gated_ceil(N, tile_columns(256, gated)) / 2);
         if (!ok(p)) p = GatedPlan{GT_256x256, 1};
         return p;
     }
     GatedPlan best{GT_256x256, 1};
     double least = -1;
-    for (int tile = direct ? 0 : GT_128x128; tile < (direct ? (int)GT_TILES : GT_128x128 + 1); ++tile) {
+    for (int tile = direct ? 0 : GT_128x128; tile < (direct ? (int)GT_MIXED : GT_128x128 + 1); ++tile) {
         const GatedTileInfo& info = direct ? kGatedTiles[tile] : kGuarded;
         const uint64_t n = gated_tiles(tile, gated, M, N, outputs);
         for (int splits = 1; splits <= (gated ? 1 : most); ++splits) {
@@ -100,6 +128,12 @@ inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t 
                               planes_us(M, N, outputs, splits);
             if (least < 0 || us < least) best = p, least = us;
         }
+    }
+    for (int fewer = 0; direct && fewer < 2; ++fewer) {
+        const GatedPlan p{GT_MIXED, 1, mixed_columns(gated, M, N, outputs, cus, fewer != 0)};
+        if (p.wide == 0 || !ok(p)) continue;
+        const double us = mixed_us(gated, M, N, steps ? steps : 1, outputs, cus, p.wide);
+        if (us < least) best = p, least = us;
     }
     if (time != nullptr) *time = least;
     return best;

@@ -27,7 +27,9 @@
 // every compute unit: 5120 x 11008 x 2048 gated 386 us (462 GFLOP, 1196 TFLOP/s;
 // cores busy in 54% of the cycles), the nn chain of its gradient 5120 x 2048 x
 // 22016 382 us (160 x 256 tiles, one round; 525 us with 256 x 256), the tn pair
-// 22016 x 2048 x 5120 380 us. Reading transposed costs nothing there: 4096^3 takes
+// 22016 x 2048 x 5120 380 us. Where 256 x 256 tiles leave a round mostly empty the
+// last columns go in 256 x 128 (gated_tiles.hpp): 5120 x 11008 x 2048 as nn 200 us
+// (1156 TFLOP/s) instead of 230. Reading transposed costs nothing there: 4096^3 takes
 // 107.8 us as nn and as tn (1274 TFLOP/s). Steps of 32 in four or five stages
 // (twice the time for a load to land) measured 111 and 120 us, so it is not the
 // loads' latency that bounds a step. Small products are bound by a fixed 5 us
@@ -66,6 +68,7 @@ struct GatedParams {
     int M, N, K;            // of one product
     int lda, ldb;           // elements between rows as they lie in memory
     int tiles_m, tiles_n;   // of one product
+    int start;              // the first tile's column
     int parts;
     int64_t low;            // tn: 0, or from A to a second A, whose product with the same B is added
     int splits;             // of the reduction's whole steps
@@ -322,7 +325,7 @@ __device__ __forceinline__ void gated_body(const GatedParams& p, uint16_t* smem,
         A0 = p.A1;
         C = p.C1;
     }
-    const int m0 = tm * BM, n0 = tn * BNO;
+    const int m0 = tm * BM, n0 = p.start + tn * BNO;
 
     f32x16 acc[FM][FN];
 #pragma unroll
@@ -501,6 +504,21 @@ gated_kernel(GatedParams p) {
     gated_body<MODE, ACT, BM, BN, WM, WN, STAGES, PLANES>(p, smem, (int)blockIdx.x, (int)blockIdx.y);
 }
 
+// GT_MIXED: p's tiles of 256 x 256, then the columns from `start` on in 256 x 128.
+template <int MODE, int ACT>
+__global__ void __launch_bounds__(512)
+mixed_kernel(GatedParams p, int wide, int start, int tiles_n) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[3 * (256 + 128) * STEP];
+    const int i = (int)blockIdx.x;
+    if (i < wide) {
+        gated_body<MODE, ACT, 256, 256, 2, 4, 2, false>(p, smem, i, 0);
+    } else {
+        p.start = start;
+        p.tiles_n = tiles_n;
+        gated_body<MODE, ACT, 256, 128, 4, 2, 3, false>(p, smem, i - wide, 0);
+    }
+}
+
 // An nn and a tn product that do not wait for each other, in one launch: the first
 // workgroups take a's tiles (split by split), the others b's. Where neither fills
 // the chip, both take the time of the longer: the gradient of 1015 x 1407 x 520
@@ -638,8 +656,20 @@ hipError_t launch_kernel(GatedParams p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int MODE, int ACT>
+hipError_t launch_mixed(GatedParams p, int columns, hipStream_t stream) {
+    constexpr bool GATED = MODE == MODE_GATED;
+    p.tiles_m = (p.M + 255) / 256;
+    p.tiles_n = columns;
+    const int rows = p.tiles_m * (MODE == MODE_TN ? p.parts : 1), start = columns * tile_columns(256, GATED);
+    const int tiles_n = start < p.N ? (p.N - start + tile_columns(128, GATED) - 1) / tile_columns(128, GATED) : 0;
+    const int wide = rows * columns;
+    mixed_kernel<MODE, ACT><<<dim3((unsigned)wide + (unsigned)rows * tiles_n), dim3(512), 0, stream>>>(p, wide, start, tiles_n);
+    return hipGetLastError();
+}
+
 template <int MODE, int ACT, bool PLANES>
-hipError_t launch_tile(const GatedParams& p, int tile, hipStream_t stream) {
+hipError_t launch_tile(const GatedParams& p, int tile, int wide, hipStream_t stream) {
     if (!p.direct) return launch_kernel<MODE, ACT, 128, 128, 2, 2, 1, PLANES>(p, stream);
     switch (tile) {
         //                                              BM   BN  WM WN ST
@@ -650,6 +680,9 @@ hipError_t launch_tile(const GatedParams& p, int tile, hipStream_t stream) {
         case GT_128x128: return launch_kernel<MODE, ACT, 128, 128, 2, 2, 2, PLANES>(p, stream);
         case GT_128x128_DEEP: return launch_kernel<MODE, ACT, 128, 128, 4, 2, 4, PLANES>(p, stream);
         case GT_64x128: return launch_kernel<MODE, ACT, 64, 128, 2, 2, 3, PLANES>(p, stream);
+        case GT_MIXED:
+            if constexpr (!PLANES) return launch_mixed<MODE, ACT>(p, wide, stream);
+            break;
         default: break;
     }
     return launch_kernel<MODE, ACT, 256, 256, 2, 4, 2, PLANES>(p, stream);
@@ -672,8 +705,8 @@ hipError_t launch_gated(const GatedProblem& p, hipStream_t stream) {
     q.lda = q.ldb = (int)p.K;
     q.parts = q.splits = 1;
     q.direct = gated_direct(p.K);
-    return p.act == BG_SILU ? launch_tile<MODE_GATED, BG_SILU, false>(q, p.tile, stream)
-                            : launch_tile<MODE_GATED, BG_GELU_TANH, false>(q, p.tile, stream);
+    return p.act == BG_SILU ? launch_tile<MODE_GATED, BG_SILU, false>(q, p.tile, p.wide, stream)
+                            : launch_tile<MODE_GATED, BG_GELU_TANH, false>(q, p.tile, p.wide, stream);
 }
 
 // Whether the product goes through planes, and its parameters.
@@ -709,9 +742,9 @@ static hipError_t launch_planes_sum(const TransposedProblem& p, hipStream_t stre
 hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream) {
     GatedParams q;
     if (!transposed_params(p, q))
-        return p.tn ? launch_tile<MODE_TN, 0, false>(q, p.tile, stream) : launch_tile<MODE_NN, 0, false>(q, p.tile, stream);
+        return p.tn ? launch_tile<MODE_TN, 0, false>(q, p.tile, p.wide, stream) : launch_tile<MODE_NN, 0, false>(q, p.tile, p.wide, stream);
     const hipError_t e =
-        p.tn ? launch_tile<MODE_TN, 0, true>(q, p.tile, stream) : launch_tile<MODE_NN, 0, true>(q, p.tile, stream);
+        p.tn ? launch_tile<MODE_TN, 0, true>(q, p.tile, p.wide, stream) : launch_tile<MODE_NN, 0, true>(q, p.tile, p.wide, stream);
     return e != hipSuccess ? e : launch_planes_sum(p, stream);
 }
 

@@ -43,12 +43,14 @@ static void inside(const void* p, uint64_t bytes) {
 namespace bg {
 int tune(int) { return g_tune; }
 hipError_t launch_gated(const GatedProblem& p, hipStream_t) {
+    CHECK(p.tile != GT_MIXED || (uint64_t)p.wide * 128 < (uint64_t)p.N + 128);
     CHECK(p.M > 0 && p.N > 0 && p.tile >= 0 && p.tile < GT_TILES && (p.G == nullptr) == (p.U == nullptr));
     ++g_launches;
     return hipSuccess;
 }
 hipError_t launch_transposed(const TransposedProblem& p, hipStream_t) {
     CHECK(p.M > 0 && p.N > 0 && p.tile >= 0 && p.tile < GT_TILES && p.splits >= 1);
+    CHECK(p.tile != GT_MIXED || (p.splits == 1 && (uint64_t)p.wide * 256 < (uint64_t)p.N + 256));
     CHECK(!(p.tn && p.tile == GT_160x256) && p.stacked >= 1 && p.M % p.stacked == 0 && p.lda >= (p.tn ? p.M / p.stacked : p.K));
     CHECK(p.splits <= (int)(p.K / 64 + 1) * (p.tn ? (p.low ? 2 : 1) : (int)p.parts));
     if (p.splits > 1 || p.stacked > 1) inside(p.planes, (uint64_t)p.splits * (p.tn ? p.parts : 1) * p.M * p.N * 4);

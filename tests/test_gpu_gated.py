@@ -8,7 +8,7 @@ from oracle import gated as og
 
 pytestmark = pytest.mark.gpu
 
-TILES = range(6)
+TILES = range(7)
 # one element, one row, less than a step, whole steps, odd everything, several
 # tiles of every size with ragged edges
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 130, 64), (64, 64, 64), (65, 127, 72), (128, 136, 128), (300, 200, 136),
@@ -45,6 +45,20 @@ def test_every_tile_gives_the_same_bits(m, n, k, tile, force):
     assert torch.equal(bg.gemm_bf16_tn(at, bt), tn)
     check_product(nn, a, bt, "nn")
     check_product(tn, a, bt, "tn")
+
+
+# 1.3 and 3.9 rounds of the widest tiles: the last columns go in narrower ones
+@pytest.mark.parametrize("m,n,k", [(1016, 22000, 1032), (2944, 10792, 1744)])
+def test_tiles_of_two_sizes_in_one_launch(m, n, k, force):
+    a, b = normal((m, k), 1.0, 1), normal((k, n), 1.0 / k ** 0.5, 2)
+    at, b0, b1 = a.t().contiguous(), b[:, :n // 2].t().contiguous(), b[:, n // 2:].t().contiguous()
+    run = lambda: (bg.gemm_bf16_nn(a, b), bg.gemm_bf16_tn(at, b), *bg.gemm_bf16_gated(a, b0, b1, save=True))
+    got = run()
+    force(bg.TUNE_TILE, 16 + 0)
+    for g, w in zip(got, run()):
+        assert torch.equal(g, w)
+    check_product(got[0], a, b, "nn")
+    check_gated(got[2], a, b0, b1, "silu", "gated")
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES + [(512, 264, 5000), (16, 64, 4096), (2048, 520, 64)])
