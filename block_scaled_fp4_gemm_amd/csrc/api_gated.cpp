@@ -138,6 +138,8 @@ GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
 }
 
 bool grad_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
+    // the sum of dA's planes: 1024 elements a workgroup in one launch
+    if (M <= kFineRows && (uint64_t)M * K >= (uint64_t)1 << 33) return false;
     return gated_shape_ok(M, N, K) && transposed_shape_ok(false, M, K, N) && transposed_shape_ok(true, N, K, M);
 }
 

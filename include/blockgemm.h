@@ -606,7 +606,8 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
  *     or smaller). It needs no initialization; calls that may run concurrently
  *     need separate ones.
  *  M == 0 gives dB0 = dB1 = 0, N == 0 gives dA = 0. Sizes as gemm_bf16_gated,
- *  gemm_bf16_nn and gemm_bf16_tn for the three products.
+ *  gemm_bf16_nn and gemm_bf16_tn for the three products, and M K < 2^33 up to 64
+ *  rows (BG_ERR_SHAPE otherwise).
  */
 bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const uint16_t* B0, const uint16_t* B1,
                                    const void* G, const void* U, int kept_type, uint16_t* dA, uint16_t* dB0, uint16_t* dB1,
@@ -679,7 +680,8 @@ typedef struct bg_w4 {
  *  MXFP4 and NVFP4 scales: the up to three bytes behind the array in its last
  *  aligned four-byte word are read too (never another word), and not used.
  *  INT4: s (sum (16 + q) x - (16 + z) sum x) per group, so an infinity in a row of X
- *  makes that row of Y NaN.
+ *  makes that row of Y NaN, and a group with (16 + z) sum |x| past FP32's range
+ *  its sum.
  */
 bg_status gemv_w4(const uint16_t* X, const bg_w4* W, uint16_t* Y, uint32_t R, uint32_t N, uint32_t K, void* stream);
 

@@ -164,6 +164,7 @@ STATUS = [
     (lambda: grad(db0=None), NULL), (lambda: grad(db1=None), NULL), (lambda: grad(dh=None), NULL),
     (lambda: grad(g=None), NULL), (lambda: grad(a=None), NULL), (lambda: grad(b0=None), NULL),
     (lambda: grad(act=3), SHAPE), (lambda: grad(kept=-1), SHAPE), (lambda: grad(k=BIG), SHAPE),
+    (lambda: grad(m=64, n=1, k=1 << 27), SHAPE), (lambda: grad(m=8, n=1, k=1 << 30), SHAPE),
     (lambda: grad(da=D + 2), ALIGN), (lambda: grad(g=G + 8), ALIGN),
     (lambda: grad(da=C), ALIAS), (lambda: grad(db0=A), ALIAS), (lambda: grad(db1=D1 + 16), ALIAS),
     (lambda: grad(da=G + 16), ALIAS),

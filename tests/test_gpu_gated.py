@@ -94,3 +94,15 @@ def test_backward(m, n, k, act, kept):
     assert n0 is None and n1 is None and torch.equal(da, grads[0])
     na, db0, db1 = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u, act=act, need_a=False)
     assert na is None and torch.equal(db0, grads[1]) and torch.equal(db1, grads[2])
+
+
+@pytest.mark.parametrize("parts", [0, 3])
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("m,n,k", [(40, 300, 600), (300, 515, 264)])
+def test_backward_of_every_tile(m, n, k, tile, parts, force):
+    a, b0, b1 = normal((m, k), 1.0, 1), normal((n, k), 1.5 / k ** 0.5, 2), normal((n, k), 1.0 / k ** 0.5, 3)
+    dh = normal((m, n), 0.01, 4)
+    _, g, u = bg.gemm_bf16_gated(a, b0, b1, save=True)
+    force(bg.TUNE_TILE, 16 * parts + tile)
+    grads = bg.gemm_bf16_gated_backward(dh, a, b0, b1, g, u)
+    check_backward(*grads, dh, a, b0, b1, g, u, "silu", f"{m}x{n}x{k} tile {tile}")
