@@ -25,6 +25,8 @@ struct Operand {
     uint64_t bytes;
 };
 
+uint32_t pitch8(uint32_t n) { return (n + 7) / 8 * 8; }
+
 // Pointers, alignment, and no output over an input or another output.
 template <size_t NI, size_t NO>
 bg_status check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
@@ -46,8 +48,6 @@ bg_status check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
     return BG_OK;
 }
 
-uint32_t pitch8(uint32_t n) { return (n + 7) / 8 * 8; }
-
 // An nn (C [M, N] of K terms, parts of them) or tn (parts outputs) product, A's
 // rows lda elements apart.
 GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t lda, uint32_t parts, uint32_t cus,
@@ -58,6 +58,35 @@ GatedPlan transposed_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t 
 }
 uint64_t planes_bytes(const GatedPlan& p, uint32_t M, uint32_t N, uint32_t outputs) {
     return p.splits > 1 ? (uint64_t)p.splits * outputs * M * N * 4 : 0;
+}
+
+// A product that the caller gives whole: its plan, the rows of its operands (copied
+// where lda or ldb is not their own), and the workspace: planes, A's copy, B's copy.
+struct ProductPlan {
+    GatedPlan plan;
+    uint32_t lda, ldb;
+    uint64_t planes, a, bytes;
+};
+ProductPlan product_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
+    const uint32_t cols = tn ? M : K, rows = tn ? K : M;
+    ProductPlan p{{}, cols, N, 0, 0, 0};
+    double us = 0;
+    p.plan = transposed_plan(tn, M, N, K, cols, 1, cus, &us);
+    // (a reduction below one step has no direct loads either way)
+    if (K >= 64 && !(gated_direct(cols) && gated_direct(N)) && gated_direct(pitch8(cols)) && gated_direct(pitch8(N)) && tune(BG_TUNE_TILE) < 0) {
+        double direct = 0;
+        const GatedPlan plan = plan_of(false, tn, true, M, N, K / 64, 1, cus, -1, &direct);
+        const uint64_t copied = (cols % 8 ? (uint64_t)rows * pitch8(cols) : 0) + (N % 8 ? (uint64_t)K * pitch8(N) : 0);
+        if (direct + aligned_copy_us(copied) < us) {
+            p.plan = plan;
+            p.lda = pitch8(cols);
+            p.ldb = pitch8(N);
+        }
+    }
+    p.planes = (planes_bytes(p.plan, M, N, 1) + 15) / 16 * 16;
+    p.a = p.lda != cols ? (uint64_t)rows * p.lda * 2 : 0;
+    p.bytes = p.planes + p.a + (p.ldb != N ? (uint64_t)K * p.ldb * 2 : 0);
+    return p;
 }
 
 bool transposed_shape_ok(bool tn, uint32_t M, uint32_t N, uint32_t K) {
@@ -71,7 +100,7 @@ bg_status transposed_workspace(bool tn, uint32_t M, uint32_t N, uint32_t K, size
     uint32_t cus = 0;
     const bg_status s = check_device(&cus);
     if (s != BG_OK) return s;
-    *bytes = M == 0 || N == 0 ? 0 : (size_t)planes_bytes(transposed_plan(tn, M, N, K, tn ? M : K, 1, cus), M, N, 1);
+    *bytes = M == 0 || N == 0 ? 0 : (size_t)product_plan(tn, M, N, K, cus).bytes;
     return BG_OK;
 }
 
@@ -85,16 +114,27 @@ bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C,
     if (s != BG_OK) return s;
     uint32_t cus = 0;
     if ((s = check_device(&cus)) != BG_OK) return s;
-    const GatedPlan plan = transposed_plan(tn, M, N, K, tn ? M : K, 1, cus);
-    const uint64_t need = planes_bytes(plan, M, N, 1);
-    if (need != 0) {
-        if (ws == nullptr || ws_bytes < need) return BG_ERR_WORKSPACE;
-        const Operand with[] = {in[0], in[1], out[0]}, planes[] = {{ws, need}};
-        if ((s = check_operands(with, planes)) != BG_OK) return s;
+    const ProductPlan plan = product_plan(tn, M, N, K, cus);
+    if (plan.bytes != 0) {
+        if (ws == nullptr || ws_bytes < plan.bytes) return BG_ERR_WORKSPACE;
+        const Operand with[] = {in[0], in[1], out[0]}, space[] = {{ws, plan.bytes}};
+        if ((s = check_operands(with, space)) != BG_OK) return s;
     }
-    return launched(launch_transposed(TransposedProblem{tn, A, nullptr, B, nullptr, C, nullptr, static_cast<float*>(ws), M, N, K,
-                                                        tn ? M : K, 1, plan.tile, plan.splits, 0, 1, plan.wide},
-                                      (hipStream_t)stream));
+    const hipStream_t st = (hipStream_t)stream;
+    const uint32_t rows = tn ? K : M, cols = tn ? M : K;
+    AlignedCopy copy{{A, B}, {}, {}, {cols, N}, {plan.lda, plan.ldb}};
+    hipError_t e = hipSuccess;
+    if (plan.lda != cols || plan.ldb != N) {
+        uint16_t* to = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + plan.planes);
+        if (plan.lda != cols) copy.rows[0] = rows, A = copy.to[0] = to;
+        if (plan.ldb != N) copy.rows[1] = K, B = copy.to[1] = to + plan.a / 2;
+        e = launch_aligned_copy(copy, st);
+    }
+    if (e == hipSuccess)
+        e = launch_transposed(TransposedProblem{tn, A, nullptr, B, nullptr, C, nullptr, static_cast<float*>(ws), M, N, K, plan.lda,
+                                                plan.ldb, 1, plan.plan.tile, plan.plan.splits, 0, 1, plan.plan.wide},
+                              st);
+    return launched(e);
 }
 
 bool gated_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
@@ -276,9 +316,9 @@ bg_status gemm_bf16_gated_backward(const uint16_t* dH, const uint16_t* A, const 
     if (!want_a && !want_b) return BG_OK;
     hipError_t e = hipSuccess;
     if (M != 0 && N != 0) e = launch_gate_grad(GateGradProblem{dH, G, U, kept_type, dG, dU, M, N, ld, act, low}, st);
-    const TransposedProblem nn{false, dG, dU, B0, B1, dA, nullptr, planes, M * plan.stacked, K, N, ld, 2, plan.nn.tile,
+    const TransposedProblem nn{false, dG, dU, B0, B1, dA, nullptr, planes, M * plan.stacked, K, N, ld, K, 2, plan.nn.tile,
                                plan.nn.splits, 0, plan.stacked, plan.nn.wide};
-    const TransposedProblem tn{true, dG, dU, A, nullptr, dB0, dB1, planes + plan.nn_planes / 4, N, K, M, ld, 2, plan.tn.tile,
+    const TransposedProblem tn{true, dG, dU, A, nullptr, dB0, dB1, planes + plan.nn_planes / 4, N, K, M, ld, K, 2, plan.tn.tile,
                                plan.tn.splits, low, 1, plan.tn.wide};
     if (plan.pair && want_a && want_b) {
         if (e == hipSuccess) e = launch_transposed_pair(nn, tn, st);

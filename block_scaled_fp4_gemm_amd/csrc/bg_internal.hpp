@@ -123,12 +123,19 @@ struct TransposedProblem {
     uint16_t *C0, *C1;
     float* planes;         // [splits][outputs][M][N], where splits or stacked > 1
     uint32_t M, N, K;
-    uint32_t lda;          // elements between A's rows
+    uint32_t lda, ldb;     // elements between the rows of A and of B
     uint32_t parts;
     int tile, splits;      // GatedPlan
     int64_t low;
     uint32_t stacked;      // 1 or 2
     uint32_t wide;         // GatedPlan
+};
+
+// [rows, ld] = [rows, cols] of two matrices (rows 0: none), ld a multiple of 8, zeros behind cols
+struct AlignedCopy {
+    const uint16_t* from[2];
+    uint16_t* to[2];
+    uint32_t rows[2], cols[2], ld[2];
 };
 
 struct GateGradProblem {
@@ -250,6 +257,7 @@ hipError_t launch_moe_route_backward(const RouteBackwardProblem& p, hipStream_t 
 
 hipError_t launch_gated(const GatedProblem& p, hipStream_t stream);
 hipError_t launch_transposed(const TransposedProblem& p, hipStream_t stream);
+hipError_t launch_aligned_copy(const AlignedCopy& p, hipStream_t stream);
 // Both in one launch: 128 x 128 tiles, direct loads, planes of their own.
 hipError_t launch_transposed_pair(const TransposedProblem& nn, const TransposedProblem& tn, hipStream_t stream);
 hipError_t launch_gate_grad(const GateGradProblem& p, hipStream_t stream);

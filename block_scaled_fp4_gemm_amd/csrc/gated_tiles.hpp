@@ -27,7 +27,7 @@ constexpr GatedTileInfo kGatedTiles[GT_TILES] = {{256, 256, 512, 9.0, 1.25, 1.72
 
 // Rows that do not start at multiples of 16 bytes: 128 x 128 tiles, every step
 // loaded through registers with checks.
-constexpr GatedTileInfo kGuarded = {128, 128, 256, 5.0, 2.4, 2.6, 6.0, 3.6};
+constexpr GatedTileInfo kGuarded = {128, 128, 256, 4.0, 5.0, 5.5, 5.0, 6.5};
 
 // Output columns of a tile of bn operand rows: a gated tile holds both products.
 constexpr int tile_columns(int bn, bool gated) { return gated ? bn / 2 : bn; }
@@ -138,6 +138,14 @@ inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t 
     if (time != nullptr) *time = least;
     return best;
 }
+
+// Operands of a product whose rows do not start at multiples of 16 bytes are copied
+// to rows that do, where the copy (elements read and written, one launch) and the
+// product with direct loads take less than the product with guarded ones: 5120 x
+// 11007 x 2048 as nn 226 us instead of 663, 2047 x 11007 x 5120 as tn 260 (1180),
+// 64 x 2047 x 5461 29 (53), 1 x 11007 x 2048 32 (36), 512 x 513 x 1024 14.2 (15.7);
+// but 300 x 301 x 303 14.8 (12.3 - 14), 30 x 1001 x 100 11.7 (9.6).
+inline double aligned_copy_us(uint64_t elements) { return 4.0 + (double)elements * 4e-6 / 4.8; }
 
 // An nn and a tn product in one launch of GT_128x128_DEEP tiles, where all their
 // workgroups run at once: the parts of each whose longer time is least, with the

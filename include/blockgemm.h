@@ -624,14 +624,15 @@ bg_status gemm_bf16_gated_backward_workspace(uint32_t M, uint32_t N, uint32_t K,
  *   dY^T X.
  * FP32 accumulation in an order fixed by the shape: repeated calls return
  * identical bits. Where the output has few tiles the reduction is split, and
- * FP32 planes in the workspace are added in a fixed order.
+ * FP32 planes in the workspace are added in a fixed order. Operands whose rows
+ * have a pitch that is not a multiple of 16 bytes are copied there to one that is
+ * where this is faster, and take a slower guarded load path otherwise.
  *
  *  workspace: device buffer of gemm_bf16_nn_workspace / gemm_bf16_tn_workspace
  *     (M, N, K) bytes, 16-byte aligned, overlapping no operand; NULL where that
  *     is 0 (BG_ERR_WORKSPACE if missing or smaller). It needs no initialization;
  *     calls that may run concurrently need separate ones.
- *  Rows of a pitch that is not a multiple of 16 bytes take a slower guarded load
- *  path. C must not overlap an input (BG_ERR_ALIAS). A launch's grid holds
+ *  C must not overlap an input (BG_ERR_ALIAS). A launch's grid holds
  *  ceil(M / 256) * ceil(N / 256) < 2^23 for nn and half as many for tn
  *  (BG_ERR_SHAPE otherwise).
  */
@@ -640,8 +641,9 @@ bg_status gemm_bf16_nn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* 
 bg_status gemm_bf16_tn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* workspace, size_t workspace_bytes, uint32_t M,
                        uint32_t N, uint32_t K, void* stream);
 
-/* Bytes of workspace gemm_bf16_nn and gemm_bf16_tn need on the current device
- * (0 where the reduction is not split), in *bytes. */
+/* Bytes of workspace gemm_bf16_nn and gemm_bf16_tn need on the current device (0
+ * where the reduction is not split and nothing copied), in *bytes (a tile override
+ * changes it: query after setting one). */
 bg_status gemm_bf16_nn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes);
 bg_status gemm_bf16_tn_workspace(uint32_t M, uint32_t N, uint32_t K, size_t* bytes);
 

@@ -61,6 +61,15 @@ hipError_t launch_transposed(const TransposedProblem& p, hipStream_t) {
     ++g_launches;
     return hipSuccess;
 }
+hipError_t launch_aligned_copy(const AlignedCopy& p, hipStream_t) {
+    for (int i = 0; i < 2; ++i) {
+        if (p.rows[i] == 0) continue;
+        CHECK(p.ld[i] % 8 == 0 && p.ld[i] >= p.cols[i] && p.ld[i] < p.cols[i] + 8);
+        inside(p.to[i], (uint64_t)p.rows[i] * p.ld[i] * 2);
+    }
+    CHECK(p.rows[0] != 0 || p.rows[1] != 0);
+    return hipSuccess;
+}
 hipError_t launch_transposed_pair(const TransposedProblem& nn, const TransposedProblem& tn, hipStream_t s) {
     CHECK(!nn.tn && tn.tn && nn.tile == GT_128x128_DEEP && tn.tile == GT_128x128_DEEP);
     // all workgroups at once, planes that do not meet

@@ -69,6 +69,20 @@ def test_transposed_products(m, n, k):
     check_product(bg.gemm_bf16_tn(at, b), a, b, f"tn {m}x{n}x{k}")
 
 
+@pytest.mark.parametrize("m,n,k", [(1015, 2087, 1001), (513, 1000, 1291), (2056, 777, 264), (77, 2047, 640), (1, 5461, 2049), (130, 71, 4097)])
+def test_rows_copied_to_aligned_ones(m, n, k):
+    """In a workspace of just the size, full of NaN."""
+    a, b = normal((m, k), 1.0, 1), normal((k, n), 1.0, 2)
+    for f, need, x in ((bg.gemm_bf16_nn, bg.gemm_bf16_nn_workspace, a), (bg.gemm_bf16_tn, bg.gemm_bf16_tn_workspace, a.t().contiguous())):
+        size = need(m, n, k)
+        copies = sum(t.shape[0] * ((t.shape[1] + 7) // 8 * 16) for t in (x, b) if t.shape[1] % 8)
+        assert size >= copies
+        buf = torch.full((size + 256,), 0xFF, device="cuda", dtype=torch.uint8)
+        got = f(x, b, workspace=buf[:size])
+        check_product(got, a, b, f"{f.__name__} {m}x{n}x{k}")
+        assert (buf[size:] == 0xFF).all() and torch.equal(f(x, b), got)
+
+
 @pytest.mark.parametrize("splits", [2, 3, 7])
 @pytest.mark.parametrize("tile", TILES)
 @pytest.mark.parametrize("m,n,k", [(130, 264, 1000), (64, 121, 448), (72, 128, 40)])
