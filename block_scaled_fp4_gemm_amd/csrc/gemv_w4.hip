@@ -113,8 +113,8 @@ __device__ __forceinline__ uint32_t bytes_at(const uint8_t* p, int64_t at, int64
     return *reinterpret_cast<const Word*>(p + from);
 }
 
-// A workgroup is KW x NW waves: wave (kw, nw) takes NR times 16 weight rows (of
-// both matrices where gated) and every KW-th stretch of SPAN elements of K. x goes
+// A workgroup is KW x NW waves: wave (kw, nw) takes 16 weight rows (of both
+// matrices where gated) and every KW-th stretch of SPAN elements of K. x goes
 // through LDS, one chunk of KW stretches at a time for all waves, double buffered;
 // the codes and scales of the next stretch are in flight in registers while one is
 // multiplied.
@@ -123,44 +123,42 @@ __device__ __forceinline__ uint32_t bytes_at(const uint8_t* p, int64_t at, int64
 // (int4: 1, 2 or 4).
 constexpr int SPAN = 4 * BLOCK;
 
-template <int FORMAT, int GB, int RP, int KW, int NW, int NR, bool GATED>
+template <int FORMAT, int GB, int RP, int KW, int NW, bool GATED>
 __global__ void __launch_bounds__(KW * NW * 64)
 gemv_w4_kernel(GemvParams p) {
-    constexpr int MATS = GATED ? 2 : 1, SETS = NR * MATS;      // set s: matrix s % MATS, rows s / MATS
+    constexpr int MATS = GATED ? 2 : 1;
     constexpr bool INT4 = FORMAT == BG_W4_INT4, EXCHANGE = INT4 && GB < 4;
-    constexpr int NT = KW * NW * 64, ROWS = 16 * NR * NW;      // weight rows of the workgroup
+    constexpr int NT = KW * NW * 64, ROWS = 16 * NW;      // weight rows of the workgroup
     constexpr int CHUNK = KW * SPAN, PITCH = CHUNK + 8;        // 16 rows of x: all banks
     constexpr int XREGS = (RP * CHUNK / 8 + NT - 1) / NT;
     constexpr int PAD = 20;                                    // floats between weight rows of the sums
-    constexpr int XBYTES = 2 * RP * PITCH * 2, SBYTES = SETS * KW * NW * 16 * PAD * 4;
+    constexpr int XBYTES = 2 * RP * PITCH * 2, SBYTES = MATS * KW * NW * 16 * PAD * 4;
     // words that hold a block's scales: mxfp4 4 bytes, nvfp4 8, int4 one per group
     constexpr int WORDS = FORMAT == BG_W4_MXFP4 ? 1 : FORMAT == BG_W4_NVFP4 ? 2 : 4 / GB;
     __shared__ __attribute__((aligned(16))) uint8_t lds[XBYTES > SBYTES ? XBYTES : SBYTES];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kw = wave % KW, nw = wave / KW;
-    const int n0 = blockIdx.x * ROWS + nw * (16 * NR), r0 = blockIdx.y * 16;
+    const int n0 = blockIdx.x * ROWS + nw * 16, r0 = blockIdx.y * 16;
     const int part = lane >> 4;
     const int rows = min(p.R - r0, RP);
     const bool zeros = INT4 && p.w[0].zeros != nullptr;
-    int row[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) row[i] = min(n0 + 16 * i + (lane & 15), p.N - 1);
+    const int row = min(n0 + (lane & 15), p.N - 1);
 
     const int spans = (p.K + SPAN - 1) / SPAN, chunks = (spans + KW - 1) / KW;
 
     struct Stage {
-        u32x4 codes[SETS][4];
+        u32x4 codes[MATS][4];
         // of block `part` of the stretch, as loaded (nothing may wait for them
         // before the next loads are issued): four bytes and a shift, or s and z
-        uint32_t scale[SETS][WORDS], more[SETS][WORDS];
+        uint32_t scale[MATS][WORDS], more[MATS][WORDS];
     };
     auto load = [&](Stage& t, int chunk) {
         const int k0 = min(chunk * KW + kw, spans - 1) * SPAN;
 #pragma unroll
-        for (int s = 0; s < SETS; ++s) {
-            const W4Operand& w = p.w[s % MATS];
-            const int64_t r = row[s / MATS];
+        for (int s = 0; s < MATS; ++s) {
+            const W4Operand& w = p.w[s];
+            const int64_t r = row;
             const uint8_t* codes = w.codes + r * (p.K / 2);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -208,7 +206,7 @@ gemv_w4_kernel(GemvParams p) {
         }
     };
 
-    f32x4 acc[SETS] = {};
+    f32x4 acc[MATS] = {};
 
     auto multiply = [&](const Stage& t, int chunk) {
         const int k0 = (chunk * KW + kw) * SPAN;
@@ -216,9 +214,9 @@ gemv_w4_kernel(GemvParams p) {
         const uint16_t* buf = reinterpret_cast<const uint16_t*>(lds) + (chunk & 1) * (RP * PITCH) +
                               min(lane & 15, RP - 1) * PITCH + kw * SPAN + (EXCHANGE ? 8 * part : 32 * part);
         // every lane gets the scales of all four blocks
-        uint32_t scale[SETS][WORDS][4];
+        uint32_t scale[MATS][WORDS][4];
 #pragma unroll
-        for (int s = 0; s < SETS; ++s)
+        for (int s = 0; s < MATS; ++s)
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) {
 #pragma unroll
@@ -235,7 +233,7 @@ gemv_w4_kernel(GemvParams p) {
             if constexpr (!INT4) {
                 const bool in = k0 + b * BLOCK + part * 32 < p.K;
 #pragma unroll
-                for (int s = 0; s < SETS; ++s) {
+                for (int s = 0; s < MATS; ++s) {
                     if constexpr (FORMAT == BG_W4_MXFP4) {
                         const uint32_t e = in ? scale[s][0][b] >> (8 * part) & 255u : 127u;
 #pragma unroll
@@ -252,24 +250,24 @@ gemv_w4_kernel(GemvParams p) {
             } else {
                 const u32x4 ones4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
                 const bf16x8 ones = __builtin_bit_cast(bf16x8, ones4);
-                uint32_t codes[SETS][4];
+                uint32_t codes[MATS][4];
 #pragma unroll
-                for (int s = 0; s < SETS; ++s) {
+                for (int s = 0; s < MATS; ++s) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) codes[s][i] = t.codes[s][b][i];
                     if constexpr (EXCHANGE) exchange(codes[s]);
                 }
 #pragma unroll
                 for (int g = 0; g < 4; g += GB) {
-                    f32x4 sum = {}, prod[SETS] = {};
+                    f32x4 sum = {}, prod[MATS] = {};
 #pragma unroll
                     for (int i = g; i < g + GB; ++i) {
                         sum = mfma16(x[i], ones, sum);
 #pragma unroll
-                        for (int s = 0; s < SETS; ++s) prod[s] = mfma16(x[i], int4_pairs(codes[s][i]), prod[s]);
+                        for (int s = 0; s < MATS; ++s) prod[s] = mfma16(x[i], int4_pairs(codes[s][i]), prod[s]);
                     }
 #pragma unroll
-                    for (int s = 0; s < SETS; ++s) {
+                    for (int s = 0; s < MATS; ++s) {
                         // past the end of K the group read is another one, perhaps infinite
                         const uint32_t h = k0 + b * BLOCK + g * 32 < p.K ? scale[s][g / GB][b] : 0u;
                         const float by = bf16_hi(h), off = 16.0f + (float)(h & 0xFFFFu);
@@ -313,18 +311,18 @@ gemv_w4_kernel(GemvParams p) {
     float* sums = reinterpret_cast<float*>(lds);
     auto at = [&](int s, int w, int n, int r) { return sums + ((s * (KW * NW) + w) * 16 + n) * PAD + r; };
 #pragma unroll
-    for (int s = 0; s < SETS; ++s) *reinterpret_cast<f32x4*>(at(s, wave, lane & 15, 4 * part)) = acc[s];
+    for (int s = 0; s < MATS; ++s) *reinterpret_cast<f32x4*>(at(s, wave, lane & 15, 4 * part)) = acc[s];
     __syncthreads();
     for (int q = tid; q < rows * ROWS; q += NT) {
-        const int n = q % ROWS, r = q / ROWS;      // weight row n: wave n / (16 NR) of N, its set n / 16 % NR
+        const int n = q % ROWS, r = q / ROWS;      // weight row n: wave n / 16 of N
         if (blockIdx.x * ROWS + n >= (unsigned)p.N) continue;
         float v[MATS];
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
-            const int s = n / 16 % NR * MATS + m, w0 = n / (16 * NR) * KW;
-            v[m] = *at(s, w0, n & 15, r);
+            const int w0 = n / 16 * KW;
+            v[m] = *at(m, w0, n & 15, r);
 #pragma unroll
-            for (int w = 1; w < KW; ++w) v[m] += *at(s, w0 + w, n & 15, r);
+            for (int w = 1; w < KW; ++w) v[m] += *at(m, w0 + w, n & 15, r);
             if constexpr (FORMAT == BG_W4_NVFP4) v[m] *= p.w[m].scale_2;
         }
         float out = v[0];
@@ -333,11 +331,11 @@ gemv_w4_kernel(GemvParams p) {
     }
 }
 
-template <int FORMAT, int GB, int RP, int KW, int NW, int NR, bool GATED>
+template <int FORMAT, int GB, int RP, int KW, int NW, bool GATED>
 hipError_t launch_kernel(const GemvParams& p, hipStream_t stream) {
-    constexpr int ROWS = 16 * NR * NW;
+    constexpr int ROWS = 16 * NW;
     const dim3 grid((unsigned)((p.N + ROWS - 1) / ROWS), (unsigned)((p.R + 15) / 16));
-    hipLaunchKernelGGL((gemv_w4_kernel<FORMAT, GB, RP, KW, NW, NR, GATED>), grid, dim3(KW * NW * 64), 0, stream, p);
+    hipLaunchKernelGGL((gemv_w4_kernel<FORMAT, GB, RP, KW, NW, GATED>), grid, dim3(KW * NW * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -361,12 +359,12 @@ hipError_t launch_rows(const GemvParams& p, uint32_t cus, hipStream_t stream) {
     const uint32_t groups = ((uint32_t)p.N + 15) / 16, spans = ((uint32_t)p.K + SPAN - 1) / SPAN;
     if constexpr (RP < 16) {
         if (spans >= 6 && groups <= (RP <= 4 && !GATED ? 2 : 1) * cus)
-            return launch_kernel<FORMAT, GB, RP, 8, 1, 1, GATED>(p, stream);
+            return launch_kernel<FORMAT, GB, RP, 8, 1, GATED>(p, stream);
     }
-    if (groups <= cus || RP <= 4 || (GATED && RP <= 8)) return launch_kernel<FORMAT, GB, RP, 4, 1, 1, GATED>(p, stream);
+    if (groups <= cus || RP <= 4 || (GATED && RP <= 8)) return launch_kernel<FORMAT, GB, RP, 4, 1, GATED>(p, stream);
     if constexpr (RP > 4 && !(GATED && RP <= 8)) {
-        if (groups <= 2 * cus) return launch_kernel<FORMAT, GB, RP, 4, 2, 1, GATED>(p, stream);
-        return launch_kernel<FORMAT, GB, RP, 2, 2, 1, GATED>(p, stream);
+        if (groups <= 2 * cus) return launch_kernel<FORMAT, GB, RP, 4, 2, GATED>(p, stream);
+        return launch_kernel<FORMAT, GB, RP, 2, 2, GATED>(p, stream);
     }
     return hipErrorInvalidValue;
 }
