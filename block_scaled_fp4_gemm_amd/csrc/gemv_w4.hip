@@ -8,7 +8,9 @@
 // instructions is free as long as both operands agree, so a lane multiplies the
 // elements it loaded. The waves of a workgroup share the K of the same weight
 // rows; their FP32 sums are added in LDS in a fixed order.
-//   mxfp4  the conversion instruction applies the scale 2^(s - 127);
+//   mxfp4  the conversion instruction applies the scale 2^(s - 127); what passes
+//          BF16 (codes of 2 and more under the bytes 253 and 254) makes the sum
+//          infinite or NaN, and such sums are computed again term by term;
 //   nvfp4  E2M1 times E4M3 is exact in BF16: FP32 product, packed;
 //   int4   the code is put into a BF16's upper mantissa bits, 16 + q, and the
 //          group's sum is s (sum (16 + q) x - (16 + z) sum x) with the sum of x
@@ -95,11 +97,19 @@ __device__ __forceinline__ bf16x8 mxfp4_values(uint32_t w, float scale) {
     return __builtin_bit_cast(bf16x8, u);
 }
 
+// Eight E2M1 codes.
+__device__ __forceinline__ void e2m1_values(uint32_t w, f32x2 (&v)[4]) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+}
+
 __device__ __forceinline__ bf16x8 nvfp4_values(uint32_t w, float scale) {
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    const u32x4 u = {pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(b.x * scale, b.y * scale),
-                     pack_bf16x2(c.x * scale, c.y * scale), pack_bf16x2(d.x * scale, d.y * scale)};
+    f32x2 v[4];
+    e2m1_values(w, v);
+    const u32x4 u = {pack_bf16x2(v[0].x * scale, v[0].y * scale), pack_bf16x2(v[1].x * scale, v[1].y * scale),
+                     pack_bf16x2(v[2].x * scale, v[2].y * scale), pack_bf16x2(v[3].x * scale, v[3].y * scale)};
     return __builtin_bit_cast(bf16x8, u);
 }
 
@@ -111,6 +121,35 @@ __device__ __forceinline__ uint32_t bytes_at(const uint8_t* p, int64_t at, int64
     const int64_t from = min(at, (size + 3) / 4 * 4 - 4);
     shift = 8 * (uint32_t)(at - from);
     return *reinterpret_cast<const Word*>(p + from);
+}
+
+// One sum of the definition, term by term in 64 bits, for those that came out
+// infinite or NaN of matrix instructions on factors in BF16, which do not hold
+// MXFP4's largest weights (4 * 2^126 and up). One thread takes it, 0.7 us for 32
+// elements of K, and a NaN ends it: rows of x that are NaN, or memory that nobody
+// wrote, cost little; one infinity in 7168 x 16384 costs 570 us.
+template <int FORMAT>
+__device__ float sum_of_terms(const GemvParams& p, const W4Operand& w, const uint16_t* x, int64_t n) {
+    const uint8_t* codes = w.codes + n * (p.K / 2);
+    double sum = 0.0;
+#pragma unroll 1
+    for (int k = 0; k < p.K && sum == sum; k += 32) {
+        const u32x4 c = *reinterpret_cast<const u32x4*>(codes + k / 2);
+        const uint32_t e = w.scales[n * (p.K / 32) + k / 32];
+        const double scale = e == 255u ? __builtin_nan("") : __builtin_bit_cast(double, (uint64_t)(e + (1023 - 127)) << 52);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k + 8 * i);
+            f32x2 v[4];
+            e2m1_values(c[i], v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum = __builtin_fma((double)v[j].x * scale, (double)bf16_lo(xv[j]), sum);
+                sum = __builtin_fma((double)v[j].y * scale, (double)bf16_hi(xv[j]), sum);
+            }
+        }
+    }
+    return (float)sum;
 }
 
 // A workgroup is KW x NW waves: wave (kw, nw) takes 16 weight rows (of both
@@ -324,6 +363,10 @@ gemv_w4_kernel(GemvParams p) {
 #pragma unroll
             for (int w = 1; w < KW; ++w) v[m] += *at(m, w0 + w, n & 15, r);
             if constexpr (FORMAT == BG_W4_NVFP4) v[m] *= p.w[m].scale_2;
+            if constexpr (FORMAT == BG_W4_MXFP4) {
+                if (!(__builtin_fabsf(v[m]) < __builtin_inff()))
+                    v[m] = sum_of_terms<FORMAT>(p, p.w[m], p.x + (int64_t)(r0 + r) * p.K, blockIdx.x * ROWS + n);
+            }
         }
         float out = v[0];
         if constexpr (GATED) out = (p.act == BG_SILU ? gate<BG_SILU>(v[0]) : gate<BG_GELU_TANH>(v[0])) * v[1];

@@ -672,7 +672,9 @@ typedef struct bg_w4 {
  * gemv_w4: Y[r,n] = bf16( sum_k X[r,k] w[n,k] ) for few rows, BF16 activations and
  * weights in 4 bits. Weights enter exactly, sums are FP32 in an order
  * fixed by the shape: repeated calls return identical bits, whatever the other
- * rows hold.
+ * rows hold. MXFP4 sums that come out infinite or NaN (a scale byte of 253 or 254
+ * with codes of 2 and more does it, whose weights BF16 does not hold) are computed
+ * again from the weights in 64 bits, at 0.7 us for 32 elements of K.
  *
  *  X: [R, K] BF16, read.  W: the weights [N, K].  Y: [R, N] BF16, written; must not
  *  overlap an input (BG_ERR_ALIAS).
