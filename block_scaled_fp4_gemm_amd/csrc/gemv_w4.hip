@@ -15,7 +15,9 @@
 //   int4   the code is put into a BF16's upper mantissa bits, 16 + q, and the
 //          group's sum is s (sum (16 + q) x - (16 + z) sum x) with the sum of x
 //          from the matrix core too, all in FP32: the errors are those of an
-//          FP32 sum whose weights are at most 31 instead of 15. Groups of less
+//          FP32 sum with weights of up to 31 beside one of 16 + z (24 without
+//          zero points, 271 at most). Sums that come out infinite or NaN are
+//          computed again here too. Groups of less
 //          than 128 elements would put several groups into one instruction;
 //          there the lanes exchange their words first (a 4 x 4 transposition
 //          over the wave's four parts), so that an instruction covers 32
@@ -124,10 +126,11 @@ __device__ __forceinline__ uint32_t bytes_at(const uint8_t* p, int64_t at, int64
 }
 
 // One sum of the definition, term by term in 64 bits, for those that came out
-// infinite or NaN of matrix instructions on factors in BF16, which do not hold
-// MXFP4's largest weights (4 * 2^126 and up). One thread takes it, 0.7 us for 32
+// infinite or NaN: of factors in BF16, which does not hold MXFP4's largest weights
+// (4 * 2^126 and up), or of int4's difference of two sums, which infinities and
+// values next to FP32's range do not survive. One thread takes it, 0.7 to 0.9 us for 32
 // elements of K, and a NaN ends it: rows of x that are NaN, or memory that nobody
-// wrote, cost little; one infinity in 7168 x 16384 costs 570 us.
+// wrote, cost 1 us; one infinity at the end of 7168 x 16384 costs 570 (int4 760) us.
 template <int FORMAT>
 __device__ float sum_of_terms(const GemvParams& p, const W4Operand& w, const uint16_t* x, int64_t n) {
     const uint8_t* codes = w.codes + n * (p.K / 2);
@@ -135,13 +138,26 @@ __device__ float sum_of_terms(const GemvParams& p, const W4Operand& w, const uin
 #pragma unroll 1
     for (int k = 0; k < p.K && sum == sum; k += 32) {
         const u32x4 c = *reinterpret_cast<const u32x4*>(codes + k / 2);
-        const uint32_t e = w.scales[n * (p.K / 32) + k / 32];
-        const double scale = e == 255u ? __builtin_nan("") : __builtin_bit_cast(double, (uint64_t)(e + (1023 - 127)) << 52);
+        double scale;
+        float zero = 8.0f;
+        if constexpr (FORMAT == BG_W4_INT4) {
+            const int64_t at = n * p.groups + k / p.group;
+            scale = bf16_lo(reinterpret_cast<const uint16_t*>(w.scales)[at]);
+            if (w.zeros != nullptr) zero = w.zeros[at];
+        } else {
+            const uint32_t e = w.scales[n * (p.K / 32) + k / 32];
+            scale = e == 255u ? __builtin_nan("") : __builtin_bit_cast(double, (uint64_t)(e + (1023 - 127)) << 52);
+        }
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k + 8 * i);
             f32x2 v[4];
-            e2m1_values(c[i], v);
+            if constexpr (FORMAT == BG_W4_INT4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = f32x2{(float)(c[i] >> 8 * j & 15u) - zero, (float)(c[i] >> (8 * j + 4) & 15u) - zero};
+            } else {
+                e2m1_values(c[i], v);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum = __builtin_fma((double)v[j].x * scale, (double)bf16_lo(xv[j]), sum);
@@ -363,7 +379,7 @@ gemv_w4_kernel(GemvParams p) {
 #pragma unroll
             for (int w = 1; w < KW; ++w) v[m] += *at(m, w0 + w, n & 15, r);
             if constexpr (FORMAT == BG_W4_NVFP4) v[m] *= p.w[m].scale_2;
-            if constexpr (FORMAT == BG_W4_MXFP4) {
+            if constexpr (FORMAT != BG_W4_NVFP4) {
                 if (!(__builtin_fabsf(v[m]) < __builtin_inff()))
                     v[m] = sum_of_terms<FORMAT>(p, p.w[m], p.x + (int64_t)(r0 + r) * p.K, blockIdx.x * ROWS + n);
             }

@@ -672,9 +672,10 @@ typedef struct bg_w4 {
  * gemv_w4: Y[r,n] = bf16( sum_k X[r,k] w[n,k] ) for few rows, BF16 activations and
  * weights in 4 bits. Weights enter exactly, sums are FP32 in an order
  * fixed by the shape: repeated calls return identical bits, whatever the other
- * rows hold. MXFP4 sums that come out infinite or NaN (a scale byte of 253 or 254
- * with codes of 2 and more does it, whose weights BF16 does not hold) are computed
- * again from the weights in 64 bits, at 0.7 us for 32 elements of K.
+ * rows hold. Sums of MXFP4 and INT4 weights that come out infinite or NaN (scale
+ * bytes of 253 and 254 with codes of 2 and more, whose weights BF16 does not hold;
+ * INT4 with infinities in X) are computed again from the weights in 64 bits, at
+ * 0.7 to 0.9 us for 32 elements of K up to the first NaN.
  *
  *  X: [R, K] BF16, read.  W: the weights [N, K].  Y: [R, N] BF16, written; must not
  *  overlap an input (BG_ERR_ALIAS).
@@ -683,9 +684,8 @@ typedef struct bg_w4 {
  *  2^22 (BG_ERR_SHAPE otherwise). All pointers 16-byte aligned (BG_ERR_ALIGN).
  *  MXFP4 and NVFP4 scales: the up to three bytes behind the array in its last
  *  aligned four-byte word are read too (never another word), and not used.
- *  INT4: s (sum (16 + q) x - (16 + z) sum x) per group, so an infinity in a row of X
- *  makes that row of Y NaN, and a group with (16 + z) sum |x| past FP32's range
- *  its sum.
+ *  INT4: the sums are s (sum (16 + q) x - (16 + z) sum x) per group, off by what
+ *  FP32 sums of 47 + z times |s x| are (z = 8 without zero points).
  */
 bg_status gemv_w4(const uint16_t* X, const bg_w4* W, uint16_t* Y, uint32_t R, uint32_t N, uint32_t K, void* stream);
 
