@@ -10,18 +10,16 @@
 // rows; their FP32 sums are added in LDS in a fixed order.
 //   mxfp4  the conversion instruction applies the scale 2^(s - 127); what passes
 //          BF16 (codes of 2 and more under the bytes 253 and 254) makes the sum
-//          infinite or NaN, and such sums are computed again term by term;
+//          infinite or NaN, and such sums are computed again (sum_of_terms);
 //   nvfp4  E2M1 times E4M3 is exact in BF16: FP32 product, packed;
 //   int4   the code is put into a BF16's upper mantissa bits, 16 + q, and the
 //          group's sum is s (sum (16 + q) x - (16 + z) sum x) with the sum of x
 //          from the matrix core too, all in FP32: the errors are those of an
 //          FP32 sum with weights of up to 31 beside one of 16 + z (24 without
-//          zero points, 271 at most). Sums that come out infinite or NaN are
-//          computed again here too. Groups of less
-//          than 128 elements would put several groups into one instruction;
-//          there the lanes exchange their words first (a 4 x 4 transposition
-//          over the wave's four parts), so that an instruction covers 32
-//          consecutive elements.
+//          zero points, 271 at most). Groups of less than 128 elements would put
+//          several groups into one instruction; there the lanes exchange their
+//          words first (a 4 x 4 transposition over the wave's four parts), so
+//          that an instruction covers 32 consecutive elements.
 //
 // Bound by the weights' bytes, and for more rows by x, which every workgroup
 // reads whole: 7168 x 16384 MXFP4 (62 MB) takes 15.1 us for one row (4.1 TB/s; the
@@ -127,10 +125,11 @@ __device__ __forceinline__ uint32_t bytes_at(const uint8_t* p, int64_t at, int64
 
 // One sum of the definition, term by term in 64 bits, for those that came out
 // infinite or NaN: of factors in BF16, which does not hold MXFP4's largest weights
-// (4 * 2^126 and up), or of int4's difference of two sums, which infinities and
-// values next to FP32's range do not survive. One thread takes it, 0.7 to 0.9 us for 32
-// elements of K, and a NaN ends it: rows of x that are NaN, or memory that nobody
-// wrote, cost 1 us; one infinity at the end of 7168 x 16384 costs 570 (int4 760) us.
+// (4 * 2^126 and up), of int4's difference of two sums, which infinities and
+// values next to FP32's range do not survive, or of nvfp4's sum before its second
+// scale. One thread takes it, 0.7 to 0.9 us for 32 elements of K, and a NaN ends
+// it: rows of x that are NaN, or memory that nobody wrote, cost 1 us; one infinity
+// at the end of 7168 x 16384 costs 570 (int4 760) us.
 template <int FORMAT>
 __device__ float sum_of_terms(const GemvParams& p, const W4Operand& w, const uint16_t* x, int64_t n) {
     const uint8_t* codes = w.codes + n * (p.K / 2);
@@ -138,13 +137,13 @@ __device__ float sum_of_terms(const GemvParams& p, const W4Operand& w, const uin
 #pragma unroll 1
     for (int k = 0; k < p.K && sum == sum; k += 32) {
         const u32x4 c = *reinterpret_cast<const u32x4*>(codes + k / 2);
-        double scale;
+        double scale = 0.0;
         float zero = 8.0f;
         if constexpr (FORMAT == BG_W4_INT4) {
             const int64_t at = n * p.groups + k / p.group;
             scale = bf16_lo(reinterpret_cast<const uint16_t*>(w.scales)[at]);
             if (w.zeros != nullptr) zero = w.zeros[at];
-        } else {
+        } else if constexpr (FORMAT == BG_W4_MXFP4) {
             const uint32_t e = w.scales[n * (p.K / 32) + k / 32];
             scale = e == 255u ? __builtin_nan("") : __builtin_bit_cast(double, (uint64_t)(e + (1023 - 127)) << 52);
         }
@@ -157,6 +156,10 @@ __device__ float sum_of_terms(const GemvParams& p, const W4Operand& w, const uin
                 for (int j = 0; j < 4; ++j) v[j] = f32x2{(float)(c[i] >> 8 * j & 15u) - zero, (float)(c[i] >> (8 * j + 4) & 15u) - zero};
             } else {
                 e2m1_values(c[i], v);
+            }
+            if constexpr (FORMAT == BG_W4_NVFP4) {
+                const f32x2 s = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w.scales[n * (p.K / 16) + k / 16 + i / 2], 1.0f, false);
+                scale = (double)s.x * w.scale_2;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -379,10 +382,8 @@ gemv_w4_kernel(GemvParams p) {
 #pragma unroll
             for (int w = 1; w < KW; ++w) v[m] += *at(m, w0 + w, n & 15, r);
             if constexpr (FORMAT == BG_W4_NVFP4) v[m] *= p.w[m].scale_2;
-            if constexpr (FORMAT != BG_W4_NVFP4) {
-                if (!(__builtin_fabsf(v[m]) < __builtin_inff()))
-                    v[m] = sum_of_terms<FORMAT>(p, p.w[m], p.x + (int64_t)(r0 + r) * p.K, blockIdx.x * ROWS + n);
-            }
+            if (!(__builtin_fabsf(v[m]) < __builtin_inff()))
+                v[m] = sum_of_terms<FORMAT>(p, p.w[m], p.x + (int64_t)(r0 + r) * p.K, blockIdx.x * ROWS + n);
         }
         float out = v[0];
         if constexpr (GATED) out = (p.act == BG_SILU ? gate<BG_SILU>(v[0]) : gate<BG_GELU_TANH>(v[0])) * v[1];

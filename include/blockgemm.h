@@ -672,9 +672,9 @@ typedef struct bg_w4 {
  * gemv_w4: Y[r,n] = bf16( sum_k X[r,k] w[n,k] ) for few rows, BF16 activations and
  * weights in 4 bits. Weights enter exactly, sums are FP32 in an order
  * fixed by the shape: repeated calls return identical bits, whatever the other
- * rows hold. Sums of MXFP4 and INT4 weights that come out infinite or NaN (scale
- * bytes of 253 and 254 with codes of 2 and more, whose weights BF16 does not hold;
- * INT4 with infinities in X) are computed again from the weights in 64 bits, at
+ * rows hold. Sums that come out infinite or NaN (MXFP4 scale bytes of 253 and 254
+ * with codes of 2 and more, whose weights BF16 does not hold; infinities in X;
+ * NVFP4 sums past FP32's range before scale_2) are computed again from the weights in 64 bits, at
  * 0.7 to 0.9 us for 32 elements of K up to the first NaN.
  *
  *  X: [R, K] BF16, read.  W: the weights [N, K].  Y: [R, N] BF16, written; must not

@@ -1,4 +1,4 @@
-"""Int4 weights beside infinities and values next to FP32's range: what the
+"""Weights in 4 bits beside infinities and values next to FP32's range: what the
 definition gives, sum of s (q - z) x, not what its rearrangement gives."""
 import pytest
 import torch
@@ -87,3 +87,17 @@ def test_infinite_scales(group, zeros):
     assert (y[:, 3] == INF).all() and (y[:, 5] == -INF).all() and y[:, 6].isnan().all()
     cols = [i for i in range(n) if i not in (3, 5, 6)]
     assert torch.equal(y[:, cols], clean[:, cols])
+
+
+def test_nvfp4_sums_past_the_range_before_the_second_scale():
+    n, k = 20, 96
+    w, v = weights(n, k, "nvfp4", 16, False, 5)
+    w, v = w._replace(scale_2=2.0 ** -30), v / 0.375 * 2.0 ** -30
+    x = (normal((2, k), 1.0, 1).double() * 2.0 ** 125).clamp(-3e38, 3e38).bfloat16()
+    size = terms(x.abs(), v.abs())
+    assert size.max() < 2.0 ** 126 and (size.min() * 2.0 ** 30).item() > 2.0 ** 128
+    want = terms(x, v)
+    same(bg.gemv_w4(x, w), want, U16 * want.abs() + sum_error(size, 2 * k), "nvfp4")
+    x[1, 40] = -INF
+    want = terms(x, v)
+    same(bg.gemv_w4(x, w), want, U16 * want.abs() + sum_error(size, 2 * k), "nvfp4, infinite")
