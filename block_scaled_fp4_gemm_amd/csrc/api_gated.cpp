@@ -89,14 +89,14 @@ ProductPlan product_plan(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t c
     return p;
 }
 
-bool transposed_shape_ok(bool tn, uint32_t M, uint32_t N, uint32_t K) {
+bool transposed_shape_ok(bool tn, uint32_t M, uint32_t N, uint32_t K, uint32_t lda) {
     return dims_ok(M, N, K) && N <= kMaxDim - 7 && M <= kMaxDim - 7 && fits(M, K, 2) && fits(K, N, 2) &&
-           fits(M, N, 64 * 4) && gated_launches(GatedPlan{GT_256x256, 1}, false, M, N, tn ? 2 : 1);
+           fits(M, N, 64 * 4) && gated_fits(gated_direct(lda) && gated_direct(N), false, M, N, tn ? 2 : 1);
 }
 
 bg_status transposed_workspace(bool tn, uint32_t M, uint32_t N, uint32_t K, size_t* bytes) {
     if (bytes == nullptr) return BG_ERR_NULL;
-    if (!transposed_shape_ok(tn, M, N, K)) return BG_ERR_SHAPE;
+    if (!transposed_shape_ok(tn, M, N, K, tn ? M : K)) return BG_ERR_SHAPE;
     uint32_t cus = 0;
     const bg_status s = check_device(&cus);
     if (s != BG_OK) return s;
@@ -106,7 +106,7 @@ bg_status transposed_workspace(bool tn, uint32_t M, uint32_t N, uint32_t K, size
 
 bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C, void* ws, size_t ws_bytes, uint32_t M,
                      uint32_t N, uint32_t K, void* stream) {
-    if (!transposed_shape_ok(tn, M, N, K)) return BG_ERR_SHAPE;
+    if (!transposed_shape_ok(tn, M, N, K, tn ? M : K)) return BG_ERR_SHAPE;
     if (M == 0 || N == 0) return BG_OK;
     const Operand in[] = {{A, (uint64_t)M * K * 2}, {B, (uint64_t)K * N * 2}};
     const Operand out[] = {{C, (uint64_t)M * N * 2}};
@@ -139,7 +139,7 @@ bg_status transposed(bool tn, const uint16_t* A, const uint16_t* B, uint16_t* C,
 
 bool gated_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
     return dims_ok(M, N, K) && N <= kMaxDim - 7 && M <= kMaxDim - 7 && K <= kMaxDim - 7 && fits(M, K, 2) && fits(N, K, 2) &&
-           fits(M, N, 4) && gated_launches(GatedPlan{GT_256x256, 1}, true, M, N, 1);
+           fits(M, N, 4) && gated_fits(gated_direct(K), true, M, N, 1);
 }
 
 // The gradient's workspace: dG and dU, each followed by its low half where M is
@@ -180,7 +180,7 @@ GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
 bool grad_shape_ok(uint32_t M, uint32_t N, uint32_t K) {
     // the sum of dA's planes: 1024 elements a workgroup in one launch
     if (M <= kFineRows && (uint64_t)M * K >= (uint64_t)1 << 33) return false;
-    return gated_shape_ok(M, N, K) && transposed_shape_ok(false, M, K, N) && transposed_shape_ok(true, N, K, M);
+    return gated_shape_ok(M, N, K) && transposed_shape_ok(false, M, K, N, pitch8(N)) && transposed_shape_ok(true, N, K, M, pitch8(N));
 }
 
 // One set of weights in 4 bits: its shape, and its operands in order.

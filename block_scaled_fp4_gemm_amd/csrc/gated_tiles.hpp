@@ -53,6 +53,14 @@ inline bool gated_launches(const GatedPlan& p, bool gated, uint32_t M, uint32_t 
     return gated_tiles(p.tile, gated, M, N, outputs) * p.splits * kGatedTiles[p.tile].threads < ((uint64_t)1 << 32);
 }
 
+// The tile that every problem may fall back to, and whether a launch holds it:
+// 256 x 256, or kGuarded's without direct loads (both bounds then).
+constexpr int gated_last_tile(bool direct) { return direct ? GT_256x256 : GT_128x128; }
+inline bool gated_fits(bool direct, bool gated, uint32_t M, uint32_t N, uint32_t outputs) {
+    return gated_launches(GatedPlan{GT_256x256, 1}, gated, M, N, outputs) &&
+           gated_launches(GatedPlan{gated_last_tile(direct), 1}, gated, M, N, outputs);
+}
+
 // n tiles of `steps` steps in rounds over the compute units.
 inline double gated_us(const GatedTileInfo& t, uint64_t n, double steps, uint32_t cus) {
     const uint64_t slots = t.pair > 0 ? 2 * (uint64_t)cus : cus;
@@ -100,21 +108,21 @@ constexpr int kMaxSplits = 16;
 
 // The tile, and the number of parts of the reduction (products without a
 // workspace: one), whose time by the table is least. Without direct loads there is
-// one tile (kGuarded). `forced` >= 0: tile forced % 16 and forced / 16 parts.
+// one tile (kGuarded, GT_128x128 by name). `forced` >= 0: tile forced % 16 and forced / 16 parts.
 inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t N, uint32_t steps, uint32_t outputs, uint32_t cus,
                          int forced, double* time = nullptr) {
     const int most = steps < 2 ? 1 : steps < (uint32_t)kMaxSplits ? (int)steps : kMaxSplits;
+    const GatedPlan last{gated_last_tile(direct), 1};
     auto ok = [&](const GatedPlan& p) {
-        return !(tn && p.tile == GT_160x256) && (p.tile == GT_256x256 || gated_launches(p, gated, M, N, outputs));
+        return !(tn && p.tile == GT_160x256) && ((p.tile == last.tile && p.splits == 1) || gated_launches(p, gated, M, N, outputs));
     };
     if (forced >= 0) {
-        GatedPlan p{forced % 16 < GT_TILES ? forced % 16 : GT_256x256, 1};
+        GatedPlan p{direct && forced % 16 < GT_TILES ? forced % 16 : last.tile, 1};
         if (!gated && forced >= 16) p.splits = forced / 16 < most ? forced / 16 : most;
         if (p.tile == GT_MIXED) p.splits = 1, p.wide = (uint32_t)(gated_ceil(N, tile_columns(256, gated)) / 2);
-        if (!ok(p)) p = GatedPlan{GT_256x256, 1};
-        return p;
+        return ok(p) ? p : last;
     }
-    GatedPlan best{GT_256x256, 1};
+    GatedPlan best = last;
     double least = -1;
     for (int tile = direct ? 0 : GT_128x128; tile < (direct ? (int)GT_MIXED : GT_128x128 + 1); ++tile) {
         const GatedTileInfo& info = direct ? kGatedTiles[tile] : kGuarded;

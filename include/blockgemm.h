@@ -579,10 +579,11 @@ typedef enum bg_activation { BG_SILU = 0, BG_GELU_TANH = 1 } bg_activation;
  *  G, U: both NULL, or [M, N] of kept_type (a bg_type), written: g and u, which
  *     the gradient takes. One of them alone is BG_ERR_NULL.
  *  act: a bg_activation (BG_ERR_SHAPE otherwise).
- *  K % 8 != 0 takes a slower guarded load path. The summation order is fixed by
+ *  K % 8 != 0 and K >= 2^22 take a slower guarded load path. The summation order is fixed by
  *  the shape: repeated calls return identical bits. Outputs overlap neither an
  *  input nor each other (BG_ERR_ALIAS). A launch's grid holds ceil(M / 256) *
- *  ceil(N / 128) < 2^23 (BG_ERR_SHAPE otherwise).
+ *  ceil(N / 128) < 2^23, and on the guarded load path ceil(M / 128) * ceil(N / 64) <
+ *  2^24 (BG_ERR_SHAPE otherwise).
  */
 bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t* B1, uint16_t* H, void* G, void* U,
                           int kept_type, int act, uint32_t M, uint32_t N, uint32_t K, void* stream);
@@ -626,15 +627,17 @@ bg_status gemm_bf16_gated_backward_workspace(uint32_t M, uint32_t N, uint32_t K,
  * identical bits. Where the output has few tiles the reduction is split, and
  * FP32 planes in the workspace are added in a fixed order. Operands whose rows
  * have a pitch that is not a multiple of 16 bytes are copied there to one that is
- * where this is faster, and take a slower guarded load path otherwise.
+ * where this is faster, and take a slower guarded load path otherwise, as rows of
+ * 2^22 elements and more do.
  *
  *  workspace: device buffer of gemm_bf16_nn_workspace / gemm_bf16_tn_workspace
  *     (M, N, K) bytes, 16-byte aligned, overlapping no operand; NULL where that
  *     is 0 (BG_ERR_WORKSPACE if missing or smaller). It needs no initialization;
  *     calls that may run concurrently need separate ones.
  *  C must not overlap an input (BG_ERR_ALIAS). A launch's grid holds
- *  ceil(M / 256) * ceil(N / 256) < 2^23 for nn and half as many for tn
- *  (BG_ERR_SHAPE otherwise).
+ *  ceil(M / 256) * ceil(N / 256) < 2^23, and with rows of an operand
+ *  that are no multiple of 16 bytes, or 2^22 elements and longer, ceil(M / 128) *
+ *  ceil(N / 128) < 2^24, for nn and half as many for tn (BG_ERR_SHAPE otherwise).
  */
 bg_status gemm_bf16_nn(const uint16_t* A, const uint16_t* B, uint16_t* C, void* workspace, size_t workspace_bytes, uint32_t M,
                        uint32_t N, uint32_t K, void* stream);
