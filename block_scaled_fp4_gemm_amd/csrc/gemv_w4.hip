@@ -371,23 +371,45 @@ gemv_w4_kernel(GemvParams p) {
 #pragma unroll
     for (int s = 0; s < MATS; ++s) *reinterpret_cast<f32x4*>(at(s, wave, lane & 15, 4 * part)) = acc[s];
     __syncthreads();
+    // The sum of output q and matrix m.
+    auto sum = [&](int q, int m) {
+        const int n = q % ROWS, r = q / ROWS, w0 = n / 16 * KW;      // weight row n: wave n / 16 of N
+        float v = *at(m, w0, n & 15, r);
+#pragma unroll
+        for (int w = 1; w < KW; ++w) v += *at(m, w0 + w, n & 15, r);
+        if constexpr (FORMAT == BG_W4_NVFP4) v *= p.w[m].scale_2;
+        return v;
+    };
+    auto store = [&](int q, const float (&v)[MATS]) {
+        float out = v[0];
+        if constexpr (GATED) out = (p.act == BG_SILU ? gate<BG_SILU>(v[0]) : gate<BG_GELU_TANH>(v[0])) * v[MATS - 1];
+        p.y[(int64_t)(r0 + q / ROWS) * p.N + blockIdx.x * ROWS + q % ROWS] = (uint16_t)pack_bf16x2(out, 0.0f);
+    };
+    auto finite = [](float v) { return __builtin_fabsf(v) < __builtin_inff(); };
+    bool again = false;
     for (int q = tid; q < rows * ROWS; q += NT) {
-        const int n = q % ROWS, r = q / ROWS;      // weight row n: wave n / 16 of N
+        if (blockIdx.x * ROWS + q % ROWS >= (unsigned)p.N) continue;
+        float v[MATS];
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+            v[m] = sum(q, m);
+            again |= !finite(v[m]);
+        }
+        store(q, v);
+    }
+    if (!again) return;
+    // Behind the stores, so that a launch without such sums does not fetch the code:
+    // 1 x 11008 x 2048 int4 gated 9.3 us, with it before the store 9.4.
+    for (int q = tid; q < rows * ROWS; q += NT) {
+        const int n = q % ROWS, r = q / ROWS;
         if (blockIdx.x * ROWS + n >= (unsigned)p.N) continue;
         float v[MATS];
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
-            const int w0 = n / 16 * KW;
-            v[m] = *at(m, w0, n & 15, r);
-#pragma unroll
-            for (int w = 1; w < KW; ++w) v[m] += *at(m, w0 + w, n & 15, r);
-            if constexpr (FORMAT == BG_W4_NVFP4) v[m] *= p.w[m].scale_2;
-            if (!(__builtin_fabsf(v[m]) < __builtin_inff()))
-                v[m] = sum_of_terms<FORMAT>(p, p.w[m], p.x + (int64_t)(r0 + r) * p.K, blockIdx.x * ROWS + n);
+            v[m] = sum(q, m);
+            if (!finite(v[m])) v[m] = sum_of_terms<FORMAT>(p, p.w[m], p.x + (int64_t)(r0 + r) * p.K, blockIdx.x * ROWS + n);
         }
-        float out = v[0];
-        if constexpr (GATED) out = (p.act == BG_SILU ? gate<BG_SILU>(v[0]) : gate<BG_GELU_TANH>(v[0])) * v[1];
-        p.y[(int64_t)(r0 + r) * p.N + blockIdx.x * ROWS + n] = (uint16_t)pack_bf16x2(out, 0.0f);
+        store(q, v);
     }
 }
 
