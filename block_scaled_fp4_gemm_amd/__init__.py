@@ -469,7 +469,8 @@ def fp4_scales_from_blocked(blocked: torch.Tensor, rows: int, k_groups: int, bat
 
 def gemm_w4a16(a: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor, scale_2: float,
                out: torch.Tensor | None = None, stream=None):
-    """C = bf16(scale_2 * (A @ deq(B)^T)): A [M,K] bf16, B [N,K/2] packed e2m1, SFB [N,K/16] e4m3fn."""
+    """C = bf16(scale_2 * (A @ deq(B)^T)): A [M,K] bf16, B [N,K/2] packed e2m1, SFB [N,K/16] e4m3fn. Made for many
+    rows: up to about 100 of them gemv_w4 takes the same weights ("nvfp4", K a multiple of 32) faster."""
     m, k = _dims(_bits16(a, "A"), 2, "A")
     n, _ = _dims(_bytes(b, "B"), 2, "B")
     if k % 16 != 0:
@@ -839,7 +840,8 @@ def gemm_bf16_gated(a: torch.Tensor, b0: torch.Tensor, b1: torch.Tensor, act: st
                     save: bool | torch.dtype = False, out: torch.Tensor | None = None, stream=None):
     """H = bf16(act(A @ B0^T) * (A @ B1^T)) for A [M,K], B0 and B1 [N,K]; act is "silu" or "gelu_tanh". With
     `save`, (H, G, U): G = A @ B0^T and U = A @ B1^T too, for gemm_bf16_gated_backward, in float32 (True) or in
-    the dtype given (torch.bfloat16: half the memory, the gradient a little less exact)."""
+    the dtype given (torch.bfloat16: half the memory, the gradient a little less exact). K % 8 != 0 is slow: pad
+    such a K with zeros where that matters."""
     kind = _activation(act)
     m, k = _dims(_bits16(a, "A"), 2, "A")
     n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
@@ -862,7 +864,7 @@ def gemm_bf16_gated_backward(dh: torch.Tensor, a: torch.Tensor, b0: torch.Tensor
                              workspace: torch.Tensor | None = None, stream=None):
     """(dA, dB0, dB1) for a gradient dH [M,N] of gemm_bf16_gated's H, with the G and U it saved; None where need_a
     or need_b is false. `workspace` is a byte tensor of gemm_bf16_gated_backward_workspace(M, N, K) bytes (allocated
-    if None)."""
+    if None). K % 8 != 0 is slow (any N is not): pad such a K with zeros where that matters."""
     kind = _activation(act)
     m, k = _dims(_bits16(a, "A"), 2, "A")
     n, _ = _dims(_bits16(b0, "B0"), 2, "B0")
@@ -940,7 +942,8 @@ def _w4(w: W4Weights, k: int, what: str):
 
 
 def gemv_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, stream=None):
-    """Y[R,N] = bf16(x[R,K] @ deq(W)^T) for few rows of bfloat16 activations (16 at a time)."""
+    """Y[R,N] = bf16(x[R,K] @ deq(W)^T) for few rows of bfloat16 activations (16 at a time; from about 128 rows
+    gemm_w4a16 is faster for "nvfp4"). K is a multiple of 32."""
     r, k = _dims(_bits16(x, "x"), 2, "x")
     held, n = _w4(w, k, "W")
     _given(out, (r, n))

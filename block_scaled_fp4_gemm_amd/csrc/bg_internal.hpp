@@ -171,8 +171,11 @@ constexpr uint32_t mx_quant_pieces(uint32_t K) { return K / 512 + (K % 512 != 0)
 constexpr uint32_t kMaxMxK = 1u << 24;     // MXFP4 products: 256 rows of K / 2 bytes stay within 32-bit offsets
 // Up to this many rows the gated block's gradient keeps 16 bits of dG and dU (two
 // BF16) instead of 8: a gradient of few rows is a sum of few of them, whose
-// roundings then show. It costs nothing there (64-row tiles are half empty, the
-// weights' bytes are the time): 32 x 11008 x 2048 in both.
+// roundings then show. A choice for accuracy (1.4 times the error at 65 rows): both
+// products run over twice the rows. Whole gradient with and without, us: 32 x 11008
+// x 2048 71 and 58 (dA 32 and 28, dB 46 and 36), 64 rows 68 and 58 (dA 37 and 31, dB
+// 38 and 33), 65 rows without 65; 32 and 64 x 1407 x 520 21.2 and 18.8, 22.0 and 19.6;
+// 32 and 64 x 4096 x 4096 57 and 53, 52.7 and 52.3.
 constexpr uint32_t kFineRows = 64;
 constexpr uint32_t kMaxGemvK = 1u << 20;      // block / group by one 32-bit multiplication
 constexpr uint32_t kMaxGemvRows = 1u << 16;   // sixteen rows of a grid's y

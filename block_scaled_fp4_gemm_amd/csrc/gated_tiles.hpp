@@ -10,7 +10,8 @@ namespace bg {
 // us: per tile; per step of 64 with few tiles on the chip, with one on every
 // compute unit, and, where two fit a unit's LDS, the tile and the step of a pair
 // (0: one workgroup fills it). Medians over the three products, 32 to 1024 tiles
-// and K 512 to 6144; the sum is within 10% of most of them.
+// and K 512 to 6144; the sum is within 10% of most of them, and 15% above the
+// largest gated products (444 us for 5120 x 11008 x 2048, which takes 386).
 struct GatedTileInfo {
     int bm, bn, threads;
     double fixed, few, full, pair_fixed, pair;
@@ -78,9 +79,10 @@ inline double gated_us(const GatedTileInfo& t, uint64_t n, double steps, uint32_
 // columns that are left go in 256 x 128 tiles, first on the units that the last
 // round leaves free. It saves most of a round that 256 x 256 tiles alone would
 // fill to less than a half: 5120 x 11008 x 2048 as nn (860 of them, 3.4 rounds)
-// 200 us, in 256 x 256 alone 248, in 256 x 128 alone 230; 2048 x 11008 x 5120 as
-// tn (344, 1.3 rounds) 200, 236, 234 us. One round less pays where the columns do
-// not divide the rounds: 12152 x 2672 x 5736 as tn 340 us, with the other rule 384.
+// 226 us, in 256 x 256 alone 241, in 256 x 128 alone 249; 2048 x 11008 x 5120 as
+// tn (344, 1.3 rounds) 229, 264, 258 us; 12152 x 2672 x 5736 as tn, where one round
+// less pays because the columns do not divide the rounds, 365, 445, 397 (all in one
+// run; cards and clocks differ by 10%).
 inline uint32_t mixed_columns(bool gated, uint32_t M, uint32_t N, uint32_t outputs, uint32_t cus, bool fewer) {
     const uint64_t column = gated_ceil(M, 256) * outputs, all = gated_ceil(N, tile_columns(256, gated));
     const uint64_t rounds = column * all / cus;
@@ -150,7 +152,7 @@ inline GatedPlan plan_of(bool gated, bool tn, bool direct, uint32_t M, uint32_t 
 // Operands of a product whose rows do not start at multiples of 16 bytes are copied
 // to rows that do, where the copy (elements read and written, one launch) and the
 // product with direct loads take less than the product with guarded ones: 5120 x
-// 11007 x 2048 as nn 226 us instead of 663, 2047 x 11007 x 5120 as tn 260 (1180),
+// 11007 x 2048 as nn 250 us instead of 712, 2047 x 11007 x 5120 as tn 291 (1736),
 // 64 x 2047 x 5461 29 (53), 1 x 11007 x 2048 32 (36), 512 x 513 x 1024 14.2 (15.7);
 // but 300 x 301 x 303 14.8 (12.3 - 14), 30 x 1001 x 100 11.7 (9.6).
 inline double aligned_copy_us(uint64_t elements) { return 4.0 + (double)elements * 4e-6 / 4.8; }

@@ -27,13 +27,14 @@
 // Bound by the matrix cores and the power they draw where there are tiles for
 // every compute unit: 5120 x 11008 x 2048 gated 386 us (462 GFLOP, 1196 TFLOP/s;
 // cores busy in 54% of the cycles), the nn chain of its gradient 5120 x 2048 x
-// 22016 382 us (160 x 256 tiles, one round; 525 us with 256 x 256), the tn pair
-// 22016 x 2048 x 5120 380 us. Where 256 x 256 tiles leave a round mostly empty the
-// last columns go in 256 x 128 (gated_tiles.hpp): 5120 x 11008 x 2048 as nn 200 us
-// (1156 TFLOP/s) instead of 230. Reading transposed costs nothing there: 4096^3 takes
-// 107.8 us as nn and as tn (1274 TFLOP/s). Steps of 32 in four or five stages
-// (twice the time for a load to land) measured 111 and 120 us, so it is not the
-// loads' latency that bounds a step. Small products are bound by a fixed 5 us
+// 22016 404 us (160 x 256 tiles, one round; 585 us with 256 x 256), the tn pair
+// 22016 x 2048 x 5120 413 us. Where 256 x 256 tiles leave a round mostly empty the
+// last columns go in 256 x 128 (gated_tiles.hpp): 5120 x 11008 x 2048 as nn 226 us
+// instead of 241. Reading transposed costs nothing there: 4096^3 takes 129 us as nn
+// and as tn. Steps of 32 in four or five stages (twice the time for a load to
+// land) cost 3 and 11% more there, so it is not the loads' latency that bounds a
+// step. These calls draw all the power there is: cards, and one card warm or
+// rested, differ by 10 to 15%. Small products are bound by a fixed 5 us
 // and 0.4 - 0.6 us a step, operands coming from the L2s at 50 - 80 bytes a ns
 // and compute unit.
 #include <type_traits>

@@ -360,6 +360,9 @@ bg_status fp4_scales_from_blocked(const uint8_t* blocked, uint8_t* plain, uint32
  *  C:   [M, N] BF16, written.
  *  K must be a multiple of 16 (BG_ERR_SHAPE otherwise); C must not overlap
  *  A, B or SFB (BG_ERR_ALIAS).
+ *  Made for many rows: up to about 100 of them gemv_w4 takes the same weights
+ *  (BG_W4_NVFP4, K % 32 == 0) faster (4096 x 7168, us: one row 8 instead of 72, 16 rows
+ *  10.5, 64 rows 38, 128 rows 73).
  */
 bg_status gemm_w4a16(const uint16_t* A, const uint8_t* B, const uint8_t* SFB, float scale_2,
                      uint16_t* C, uint32_t M, uint32_t N, uint32_t K, void* stream);
@@ -567,6 +570,7 @@ bg_status moe_route_backward(const void* logits, int logits_type, const int32_t*
  * The gated MLP block: act(A B0^T) * (A B1^T), elementwise, and its gradient.
  *   silu:       act(g) = g s(g),                               s(z) = 1 / (1 + e^-z)
  *   gelu_tanh:  act(g) = g s(2 sqrt(2 / pi) (g + 0.044715 g^3))   (the tanh form of gelu)
+ * s is 0 where e^-z passes FP32's range (z < -88.7; |act(g)| is below 2^-120 there).
  */
 typedef enum bg_activation { BG_SILU = 0, BG_GELU_TANH = 1 } bg_activation;
 
@@ -579,8 +583,9 @@ typedef enum bg_activation { BG_SILU = 0, BG_GELU_TANH = 1 } bg_activation;
  *  G, U: both NULL, or [M, N] of kept_type (a bg_type), written: g and u, which
  *     the gradient takes. One of them alone is BG_ERR_NULL.
  *  act: a bg_activation (BG_ERR_SHAPE otherwise).
- *  K % 8 != 0 and K >= 2^22 take a slower guarded load path. The summation order is fixed by
- *  the shape: repeated calls return identical bits. Outputs overlap neither an
+ *  K % 8 != 0 and K >= 2^22 take a slower guarded load path (5120 x 11008 x 2047 takes
+ *  2.5 times as long as x 2048): pad such a K with zeros where that matters. The
+ *  summation order is fixed by the shape: repeated calls return identical bits. Outputs overlap neither an
  *  input nor each other (BG_ERR_ALIAS). A launch's grid holds ceil(M / 256) *
  *  ceil(N / 128) < 2^23, and on the guarded load path ceil(M / 128) * ceil(N / 64) <
  *  2^24 (BG_ERR_SHAPE otherwise).
@@ -599,13 +604,16 @@ bg_status gemm_bf16_gated(const uint16_t* A, const uint16_t* B0, const uint16_t*
  *     The roundings of dG and dU are the only ones between FP32 sums with G and U
  *     in FP32: a gradient is then about 1.4 times as far from the exact one (in
  *     the mean) as its own rounding to BF16; kept in BF16, half the memory, 1.8
- *     times. Up to 64 rows dG and dU enter as two BF16 each, 16 bits of them.
+ *     times. Up to 64 rows dG and dU enter as two BF16 each, 16 bits of them, which
+ *     takes up to a quarter longer than BF16 alone.
  *  dA: [M, K] or NULL (not wanted; B0 and B1 are then not read).
  *  dB0, dB1: [N, K], or both NULL (A is then not read).
  *  workspace: device buffer of gemm_bf16_gated_backward_workspace(M, N, K) bytes,
  *     16-byte aligned, not overlapping any operand (BG_ERR_WORKSPACE if missing
  *     or smaller). It needs no initialization; calls that may run concurrently
  *     need separate ones.
+ *  K % 8 != 0 and K >= 2^22: the products take the guarded load path (5120 x 11008 x
+ *  2047 takes five times as long as x 2048): pad such a K with zeros. Any N is fast.
  *  M == 0 gives dB0 = dB1 = 0, N == 0 gives dA = 0. Sizes as gemm_bf16_gated,
  *  gemm_bf16_nn and gemm_bf16_tn for the three products, and M K < 2^33 up to 64
  *  rows (BG_ERR_SHAPE otherwise).
@@ -677,14 +685,15 @@ typedef struct bg_w4 {
  * fixed by the shape: repeated calls return identical bits, whatever the other
  * rows hold. Sums that come out infinite or NaN (MXFP4 scale bytes of 253 and 254
  * with codes of 2 and more, whose weights BF16 does not hold; infinities in X;
- * NVFP4 sums past FP32's range before scale_2) are computed again from the weights in 64 bits, at
- * 0.7 to 0.9 us for 32 elements of K up to the first NaN.
+ * NVFP4 sums past FP32's range before scale_2) are computed again from the
+ * weights in 64 bits, at 0.7 to 0.9 us for 32 elements of K up to the first NaN.
  *
  *  X: [R, K] BF16, read.  W: the weights [N, K].  Y: [R, N] BF16, written; must not
  *  overlap an input (BG_ERR_ALIAS).
  *  Made for up to 16 rows; more are taken 16 at a time, the weights read again
- *  for each (R <= 65536). K % 32 == 0, K <= 2^20 and a grid of ceil(N / 16) * ceil(R / 16) <
- *  2^22 (BG_ERR_SHAPE otherwise). All pointers 16-byte aligned (BG_ERR_ALIGN).
+ *  for each (R <= 65536; from about 128 rows gemm_w4a16 is faster for NVFP4).
+ *  K % 32 == 0, K <= 2^20 and a grid of ceil(N / 16) * ceil(R / 16) < 2^22
+ *  (BG_ERR_SHAPE otherwise). All pointers 16-byte aligned (BG_ERR_ALIGN).
  *  MXFP4 and NVFP4 scales: the up to three bytes behind the array in its last
  *  aligned four-byte word are read too (never another word), and not used.
  *  INT4: the sums are s (sum (16 + q) x - (16 + z) sum x) per group, off by what
